@@ -11,7 +11,9 @@ Entry points: ``zs_flatten_plan`` (flat layout, rank shards, buckets),
 ``zs_gather_assemble`` (the AllGather's result and per-tensor views); the
 FSDP2 row layout (``zs_rows_plan``, ``zs_unshard``, ``zs_shard_rows``);
 clipping, accumulation, and the sharded checkpoint (``zs_checkpoint_save``,
-``zs_checkpoint_load``: host file I/O of host- or device-resident state).
+``zs_checkpoint_load``: host file I/O of host- or device-resident state); the
+losses over vocabulary rows that make the gradients (``zs_token_logprobs``,
+``zs_distill_loss`` and their gradients).
 """
 from __future__ import annotations
 
@@ -37,13 +39,15 @@ ZS_ERR_IO, ZS_ERR_CORRUPT = -8, -9
 ZS_BF16, ZS_FP32, ZS_FP24 = 0, 1, 2
 ELEM_BYTES = {ZS_BF16: 2, ZS_FP32: 4, ZS_FP24: 3}
 ZS_MAX_WORLD = 1024
+ZS_MAX_VOCAB, ZS_MAX_TOP, ZS_MAX_TEACHER = 1 << 20, 128, 256
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-fmad=false", "-prec-div=true",
               "-prec-sqrt=true", "-ftz=false", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-pthread", "-I/usr/local/cuda/include"]
-CUDA_SOURCES = ["shard_step.cu", "gather.cu", "clip.cu", "accum.cu", "rows.cu", "ckpt.cu"]
-HOST_SOURCES = ["api.cpp", "plan.cpp", "checkpoint.cpp", "trace.cpp"]
+CUDA_SOURCES = ["shard_step.cu", "gather.cu", "clip.cu", "accum.cu", "rows.cu", "ckpt.cu",
+                "losses.cu"]
+HOST_SOURCES = ["api.cpp", "plan.cpp", "checkpoint.cpp", "trace.cpp", "losses_api.cpp"]
 
 
 # ----------------------------------------------------------------- build ----
@@ -150,6 +154,17 @@ EXPORTS = {
     "zs_checkpoint_release_staging": ([], ctypes.c_int),
     "zs_set_trace": ([ctypes.c_char_p], ctypes.c_int),
     "zs_trace_first_divergence": ([_P, _I32, _P, ctypes.c_char_p, _I64], ctypes.c_int),
+    "zs_token_logprobs": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_double, _P, _P, _P,
+                           _I32, _P, _P, _P], ctypes.c_int),
+    "zs_token_logprobs_grad": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, ctypes.c_double, _P, _P,
+                                _P, _P, _P, _I64, _P], ctypes.c_int),
+    "zs_distill_loss": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _I32, _P,
+                         ctypes.c_double, _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "zs_distill_grad": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _I32, _P,
+                         ctypes.c_double, _P, _P, _P, _P, _P, _P, _I64, _P], ctypes.c_int),
+    "zs_distill_loss_grad": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _I32, _P,
+                              ctypes.c_double, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
+                             ctypes.c_int),
     "zs_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "zs_last_error": ([], ctypes.c_char_p),
     "zs_check_device_error": ([_P], ctypes.c_int),
@@ -515,6 +530,123 @@ def zs_gather_assemble(plan, rank, shard_srcs, full_flat, param_dtype, stream=No
     if views is None:  # row-sharded: the buffer is rank-major; see zs_unshard
         return None
     return [v or 0 for v in list(views)[:plan.n_params]]
+
+
+def _rows_ptr(x, rows, vocab, stride, dtype, fn, name):
+    """Address of ``rows`` x ``vocab`` elements whose rows start ``stride``
+    elements apart: a dense buffer, or a 2-D tensor with dense rows."""
+    if x is None or isinstance(x, int):
+        return x
+    size = ELEM_BYTES.get(dtype, 0)
+    if hasattr(x, "data_ptr") and not x.is_contiguous():
+        if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != stride \
+                or x.element_size() != size:
+            raise ValueError(f"{fn}: {name} must have dense rows, {stride} elements apart")
+        if x.shape[0] < rows or x.shape[1] < vocab:
+            raise ValueError(f"{fn}: {name} is {tuple(x.shape)}, the call needs {(rows, vocab)}")
+        return x.data_ptr()
+    if rows > 0:
+        _need(x, ((rows - 1) * stride + vocab) * size, fn, name)
+    return _ptr(x)
+
+
+def _rows_sizes(fn, rows, *named):
+    """(name, buffer, bytes per row) of the per-row buffers of a loss call."""
+    for name, x, nbytes in named:
+        if x is not None and not isinstance(x, int) and x.nbytes < rows * nbytes:
+            raise ValueError(f"{fn}: {name} holds {x.nbytes} bytes, the call needs "
+                             f"{rows * nbytes}")
+
+
+def zs_token_logprobs(logits, dtype, rows, vocab, row_stride, targets, temperature=1.0,
+                      logprob=None, entropy=None, lse=None, top_k=0, top_ids=None,
+                      top_logprobs=None, stream=None):
+    """Enqueue, for each row of ``logits`` (``rows`` x ``vocab``, rows
+    ``row_stride`` elements apart), the log probability of ``targets[r]`` (int64;
+    negative = none), the entropy, the log-sum-exp and the ``top_k`` most likely
+    ids (int32) with their log probabilities; fp32 outputs, None = not wanted."""
+    fn = "zs_token_logprobs"
+    _rows_sizes(fn, rows, ("targets", targets, 8), ("logprob", logprob, 4),
+                ("entropy", entropy, 4), ("lse", lse, 4), ("top_ids", top_ids, 4 * top_k),
+                ("top_logprobs", top_logprobs, 4 * top_k))
+    _check(lib().zs_token_logprobs(
+        _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
+        row_stride, _ptr(targets), temperature, _ptr(logprob), _ptr(entropy), _ptr(lse), top_k,
+        _ptr(top_ids), _ptr(top_logprobs), _stream(stream)))
+
+
+def zs_token_logprobs_grad(logits, dtype, rows, vocab, row_stride, targets, temperature, lse,
+                           entropy, d_logprob, d_entropy, d_logits, grad_stride, stream=None):
+    """Enqueue the gradient of ``zs_token_logprobs``' logprob and entropy into
+    ``d_logits`` (the logits' dtype; may be the logits themselves)."""
+    fn = "zs_token_logprobs_grad"
+    _rows_sizes(fn, rows, ("targets", targets, 8), ("lse", lse, 4), ("entropy", entropy, 4),
+                ("d_logprob", d_logprob, 4), ("d_entropy", d_entropy, 4))
+    _check(lib().zs_token_logprobs_grad(
+        _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
+        row_stride, _ptr(targets), temperature, _ptr(lse), _ptr(entropy), _ptr(d_logprob),
+        _ptr(d_entropy), _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"),
+        grad_stride, _stream(stream)))
+
+
+def _teacher_sizes(fn, rows, ids, logits, dtype, k, lse):
+    _rows_sizes(fn, rows, ("teacher_ids", ids, 4 * k),
+                ("teacher_logits", logits, ELEM_BYTES.get(dtype, 0) * k),
+                ("teacher_lse", lse, 4))
+
+
+def zs_distill_loss(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
+                    teacher_dtype, teacher_k, teacher_lse, temperature, targets=None, loss=None,
+                    lse=None, logprob=None, hard_lse=None, stream=None):
+    """Enqueue the distillation loss of each row against the teacher's
+    ``teacher_k`` recorded entries (int32 ids, negative = unused; logits of
+    ``teacher_dtype``), and with ``targets`` the hard labels' log probability."""
+    fn = "zs_distill_loss"
+    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
+    _rows_sizes(fn, rows, ("targets", targets, 8), ("loss", loss, 4), ("lse", lse, 4),
+                ("logprob", logprob, 4), ("hard_lse", hard_lse, 4))
+    _check(lib().zs_distill_loss(
+        _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
+        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
+        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(loss), _ptr(lse), _ptr(logprob),
+        _ptr(hard_lse), _stream(stream)))
+
+
+def zs_distill_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
+                    teacher_dtype, teacher_k, teacher_lse, temperature, targets, lse, hard_lse,
+                    d_loss, d_logprob, d_logits, grad_stride, stream=None):
+    """Enqueue the gradient of ``zs_distill_loss``' loss and logprob into
+    ``d_logits`` (the logits' dtype; may be the logits themselves)."""
+    fn = "zs_distill_grad"
+    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
+    _rows_sizes(fn, rows, ("targets", targets, 8), ("lse", lse, 4), ("hard_lse", hard_lse, 4),
+                ("d_loss", d_loss, 4), ("d_logprob", d_logprob, 4))
+    _check(lib().zs_distill_grad(
+        _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
+        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
+        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(lse), _ptr(hard_lse), _ptr(d_loss),
+        _ptr(d_logprob), _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"),
+        grad_stride, _stream(stream)))
+
+
+def zs_distill_loss_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
+                         teacher_dtype, teacher_k, teacher_lse, temperature, targets, d_loss,
+                         d_logprob, loss, lse, logprob, hard_lse, d_logits, grad_stride,
+                         stream=None):
+    """``zs_distill_loss`` and its gradient in one call, the logits read from
+    HBM once; ``teacher_k`` = 0: cross entropy of the targets alone."""
+    fn = "zs_distill_loss_grad"
+    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
+    _rows_sizes(fn, rows, ("targets", targets, 8), ("loss", loss, 4), ("lse", lse, 4),
+                ("logprob", logprob, 4), ("hard_lse", hard_lse, 4), ("d_loss", d_loss, 4),
+                ("d_logprob", d_logprob, 4))
+    _check(lib().zs_distill_loss_grad(
+        _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
+        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
+        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(d_loss), _ptr(d_logprob),
+        _ptr(loss), _ptr(lse), _ptr(logprob), _ptr(hard_lse),
+        _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"), grad_stride,
+        _stream(stream)))
 
 
 def _io_stream(stream):

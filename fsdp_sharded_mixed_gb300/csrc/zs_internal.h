@@ -139,6 +139,43 @@ cudaError_t launch_block_hash(const void* data, int64_t bytes, int64_t first_blo
                               cudaStream_t stream);
 int block_hash_parts(int64_t blocks, int64_t block_bytes);
 
+// Losses over vocabulary rows and their gradients (losses.cu). The entry points
+// (losses_api.cpp) fill what a call uses and leave the rest zero; the launchers
+// assume validated input.
+struct VocabLaunch {
+  const void* logits;      // row r at element r * row_stride
+  zs_dtype dtype;
+  int64_t rows, vocab, row_stride;
+  double temperature;
+  const int64_t* targets;  // or NULL
+  float* logprob;          // outputs; each may be NULL
+  float* entropy;
+  float* lse;
+  float* loss;
+  float* hard_lse;
+  int32_t top_k;
+  int32_t* top_ids;
+  float* top_logprobs;
+  bool distill;            // logprob and d_logprob are those of hard labels, at T = 1
+  int32_t teacher_k;       // 0: no teacher record
+  const int32_t* teacher_ids;
+  const void* teacher_logits;
+  zs_dtype teacher_dtype;
+  const float* teacher_lse;  // or NULL: q normalised over the record
+  const float* in_lse;       // gradient calls: what the forward call left
+  const float* in_entropy;
+  const float* in_hard_lse;
+  const float* d_loss;       // upstream gradients; each may be NULL (zero)
+  const float* d_logprob;
+  const float* d_entropy;
+  void* d_logits;            // NULL: forward only
+  int64_t grad_stride;
+};
+// Statistics and losses of each row, and with d_logits the gradient as well.
+cudaError_t launch_vocab_loss(const VocabLaunch& a, cudaStream_t stream);
+// The gradient from the forward call's normalisers.
+cudaError_t launch_vocab_grad(const VocabLaunch& a, cudaStream_t stream);
+
 // Argument checks of the C-ABI layer, for the other host translation units:
 // device-resident on the current device and (where the driver can tell)
 // [p, p + bytes) inside one allocation.

@@ -37,6 +37,9 @@ extern "C" {
 #endif
 
 #define ZS_MAX_WORLD 1024
+#define ZS_MAX_VOCAB 1048576 /* columns of a row of logits */
+#define ZS_MAX_TOP 128       /* top alternatives of a token */
+#define ZS_MAX_TEACHER 256   /* entries of a teacher's record for a token */
 
 typedef enum {
   ZS_OK = 0,
@@ -453,6 +456,113 @@ zs_status zs_set_trace(const char* path);
  * fit. n_paths >= 2. ZS_ERR_IO if a file cannot be read. */
 zs_status zs_trace_first_divergence(const char* const* paths, int32_t n_paths, int64_t* seq_out,
                                     char* detail, int64_t detail_bytes);
+
+/* ---------------------------------------------------------------------------
+ * Losses over vocabulary rows and their gradients: the end of the model that
+ * makes the gradients the shard step consumes. The pages take the gradient as
+ * given ("backward" in every step sequence they print) and have no counterpart.
+ *
+ * Common arguments:
+ *   logits, dtype     rows x vocab logits z, ZS_BF16 or ZS_FP32; row r starts
+ *                     at element r * row_stride (row_stride >= vocab). Only the
+ *                     type's own alignment is needed, for these and for every
+ *                     other buffer of these calls.
+ *   vocab             1..ZS_MAX_VOCAB. rows 0..2^31-1; with rows == 0 the call
+ *                     succeeds and touches nothing.
+ *   targets           int64 [rows] token ids; a negative id (ignore_index) is a
+ *                     row without a token: its logprob is 0 and d_logprob is
+ *                     taken as 0. An id >= vocab gives logprob NaN, counts as
+ *                     no token in the gradient, and sets the device error word
+ *                     (zs_check_device_error: ZS_ERR_RANGE).
+ *   temperature       T, finite and > 0. With y = z / T: lse = ln sum_j exp(y_j),
+ *                     ln p_j = y_j - lse.
+ *   Masked logits are -infinity (p = 0, and 0 ln 0 = 0) or any finite low value.
+ *   A row masked throughout has lse = -infinity, logprob -infinity, entropy 0
+ *   and an all-zero gradient. A NaN or +infinity makes the row's statistics NaN.
+ *   Sums, maxima and statistics are fp32; a bf16 gradient is rounded once, to
+ *   nearest even. Results do not depend on timing: the same call gives the same
+ *   bits. d_logits (dtype of the logits, row r at r * grad_stride) may be the
+ *   logits themselves with the same stride; any other overlap of an output is
+ *   ZS_ERR_INVAL. Elements between vocab and the strides are not touched.
+ * Errors: ZS_ERR_INVAL (NULL, dtype, temperature, overlap, not device memory),
+ * ZS_ERR_RANGE (sizes), ZS_ERR_ALIGN, ZS_ERR_CUDA.
+ *
+ * zs_token_logprobs — log probabilities of given tokens, with the entropy and
+ * the top alternatives of each row.
+ *   logprob [rows]    ln p of the target; needs targets. Optional (NULL), as
+ *   entropy [rows]    -sum_j p_j ln p_j, and
+ *   lse [rows]        are; at least one output is given.
+ *   top_k             0..min(vocab, ZS_MAX_TOP). top_ids int32 and top_logprobs
+ *                     fp32 [rows, top_k]: the top_k largest logits' ids and ln p,
+ *                     largest first, equal logits (and -0 and +0) lowest id
+ *                     first; NaN logits rank above all numbers.
+ * ------------------------------------------------------------------------- */
+zs_status zs_token_logprobs(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
+                            int64_t row_stride, const int64_t* targets, double temperature,
+                            float* logprob, float* entropy, float* lse, int32_t top_k,
+                            int32_t* top_ids, float* top_logprobs, void* cuda_stream);
+/* zs_token_logprobs_grad — the gradient of logprob and entropy:
+ *   d_z_j = (1/T) (a (delta_jt - p_j) - b p_j (ln p_j + H))
+ * with a = d_logprob, b = d_entropy (fp32 [rows], either may be NULL = 0, not
+ * both), p_j = exp(y_j - lse) and lse, entropy (H; needed with d_entropy) as the
+ * forward call left them. A row with a = b = 0 gets an all-zero gradient
+ * whatever its logits hold. The top alternatives have no gradient. */
+zs_status zs_token_logprobs_grad(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
+                                 int64_t row_stride, const int64_t* targets, double temperature,
+                                 const float* lse, const float* entropy, const float* d_logprob,
+                                 const float* d_entropy, void* d_logits, int64_t grad_stride,
+                                 void* cuda_stream);
+/* zs_distill_loss — distillation from a teacher's top logits:
+ *   loss = sum_k q_k (ln q_k - ln p_{id_k})            (0 where q_k = 0)
+ *   teacher_k         K, 0..ZS_MAX_TEACHER (0: no teacher; loss must be NULL).
+ *   teacher_ids       int32 [rows, K]; a negative id is a record's unused entry.
+ *                     An id >= vocab counts as unused and sets the device error
+ *                     word. Repeated ids add up.
+ *   teacher_logits    teacher_dtype (ZS_BF16 or ZS_FP32) [rows, K]: t_k.
+ *   teacher_lse       NULL: q is the softmax of t_k / T over the row's entries;
+ *                     else fp32 [rows], the teacher's own ln sum exp(t / T) over
+ *                     its whole vocabulary: q_k = exp(t_k / T - teacher_lse),
+ *                     whose sum is below 1. (The log probabilities that
+ *                     zs_token_logprobs recorded serve as t_k at T = 1, with
+ *                     zeros as teacher_lse.)
+ *   targets           NULL, or hard labels: logprob [rows] = ln p of the target
+ *                     at T = 1, and hard_lse [rows] = lse at T = 1.
+ * loss and lse (at T) fp32 [rows]. Each output may be NULL, not all. A row
+ * without teacher entries has loss 0; an entry with q_k > 0 on a masked logit
+ * makes the loss +infinity. */
+zs_status zs_distill_loss(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t row_stride, const int32_t* teacher_ids,
+                          const void* teacher_logits, zs_dtype teacher_dtype, int32_t teacher_k,
+                          const float* teacher_lse, double temperature, const int64_t* targets,
+                          float* loss, float* lse, float* logprob, float* hard_lse,
+                          void* cuda_stream);
+/* zs_distill_grad — the gradient of loss and of the hard labels' logprob:
+ *   d_z_j = (w/T) (Q p_j - sum_{k: id_k = j} q_k) + h (delta_jt - p1_j)
+ * with Q = sum_k q_k, w = d_loss, h = d_logprob (fp32 [rows], either may be
+ * NULL = 0, not both; d_logprob needs targets), p from lse and p1 (the softmax
+ * at T = 1) from hard_lse, both as the forward call left them (hard_lse needed
+ * with d_logprob; lse with d_loss). A row with w = h = 0 gets an all-zero
+ * gradient whatever its logits hold. */
+zs_status zs_distill_grad(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t row_stride, const int32_t* teacher_ids,
+                          const void* teacher_logits, zs_dtype teacher_dtype, int32_t teacher_k,
+                          const float* teacher_lse, double temperature, const int64_t* targets,
+                          const float* lse, const float* hard_lse, const float* d_loss,
+                          const float* d_logprob, void* d_logits, int64_t grad_stride,
+                          void* cuda_stream);
+/* zs_distill_loss_grad — zs_distill_loss and zs_distill_grad in one call, for
+ * training steps whose upstream gradients (a loss weight per token) are known
+ * before the loss: the logits cross HBM once. With teacher_k = 0 it is the
+ * cross entropy of the hard labels and its gradient. The outputs loss, lse,
+ * logprob and hard_lse may each be NULL. */
+zs_status zs_distill_loss_grad(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
+                               int64_t row_stride, const int32_t* teacher_ids,
+                               const void* teacher_logits, zs_dtype teacher_dtype,
+                               int32_t teacher_k, const float* teacher_lse, double temperature,
+                               const int64_t* targets, const float* d_loss,
+                               const float* d_logprob, float* loss, float* lse, float* logprob,
+                               float* hard_lse, void* d_logits, int64_t grad_stride,
+                               void* cuda_stream);
 
 /* Diagnostics. */
 const char* zs_status_string(zs_status status);
