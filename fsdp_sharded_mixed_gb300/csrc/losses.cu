@@ -36,8 +36,7 @@ struct RowArgs {
   int32_t vocab, top_k, teacher_k;
   bool teacher_bf16;
   bool distill;   // targets are hard labels at T = 1
-  bool hard_own;  // T != 1, and the hard labels' softmax is wanted as well
-  float inv_t, scale;                 // 1/T, log2(e)/T
+  float inv_t, scale, slack;  // 1/T, log2(e)/T, how far logits may exceed a reference
   const int64_t* targets;
   const int32_t* teacher_ids;
   const void* teacher_logits;
@@ -52,6 +51,197 @@ __device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 // The gradient's one rounding to fewer bits: to nearest even.
 __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// ---- the row in 32-byte chunks -------------------------------------------------
+// A chunk is one thread's widest load, aligned in memory: 16 bf16 or 8 fp32
+// logits. Rows start at any element (an odd vocabulary's do), so a row is a
+// head of single elements up to the first boundary, whole chunks, and a tail.
+constexpr int kChunkBytes = 32;
+constexpr int kWords = kChunkBytes / 4;
+template <typename T>
+constexpr int kPer = kChunkBytes / (int)sizeof(T);
+
+struct Span {
+  int head, body, tail;  // elements, chunks, elements
+};
+template <typename T>
+__device__ __forceinline__ Span span_of(const T* z, int V) {
+  const int head = min(V, (int)((0 - (uintptr_t)z) % kChunkBytes / sizeof(T)));
+  const int body = (V - head) / kPer<T>;
+  return {head, body, V - head - body * kPer<T>};
+}
+
+__device__ __forceinline__ void load_chunk(uint32_t* w, const void* p) {
+  asm volatile("ld.global.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+// Elements 2i and 2i+1 of a chunk.
+__device__ __forceinline__ float2 pair_of(const uint32_t* w, int i, __nv_bfloat16) {
+  return {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)};
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t* w, int i, float) {
+  return {__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])};
+}
+// The chunk's maximum (NaN if it holds one); bf16 maxima two at a time.
+__device__ __forceinline__ float max_of(const uint32_t* w, __nv_bfloat16) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(w);
+#pragma unroll
+  for (int i = 1; i < kWords; ++i)
+    m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(w + i));
+  return __bfloat162float(__hmax_nan(m.x, m.y));
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  return m;
+}
+__device__ __forceinline__ float max_of(const uint32_t* w, float) {
+  float m = __uint_as_float(w[0]);
+#pragma unroll
+  for (int i = 1; i < kWords; ++i) m = max_nan(m, __uint_as_float(w[i]));
+  return m;
+}
+
+// 2^x to 2 units in the last place; results below the normal range become 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+  return e;
+}
+// A log2 weight that is 2^-10000 = 0 rather than 2^-inf: 0 * -inf is not 0.
+__device__ __forceinline__ float clamped(float d) { return fmaxf(d, -1e4f); }
+
+// ---- one pass over the row ------------------------------------------------------
+// S and U (and S1, the sum at T = 1) relative to a reference logit m that
+// follows the maximum: it moves only when a chunk exceeds it by more than 8
+// powers of two, so that the sums are rescaled a few times a row and no e
+// exceeds 2^8. m = -inf until a finite logit was seen (ref is 0 meanwhile).
+template <bool ENTROPY, bool OWN>
+struct Stats {
+  float m = -INFINITY, ref = 0.0f, limit = -INFINITY;
+  float2 s = {0.0f, 0.0f}, u = {0.0f, 0.0f}, s1 = {0.0f, 0.0f};
+
+  __device__ __forceinline__ void move_to(float to, float scale, float slack) {
+    const float delta = limit == -INFINITY ? -1e4f : clamped((ref - to) * scale);
+    const float f = exp2_fast(delta);
+    if (ENTROPY) {
+      u.x = f * fmaf(s.x, delta, u.x);
+      u.y = f * fmaf(s.y, delta, u.y);
+    }
+    s.x *= f;
+    s.y *= f;
+    if (OWN) {
+      const float f1 = limit == -INFINITY ? 0.0f : exp2_fast((ref - to) * kLog2e);
+      s1.x *= f1;
+      s1.y *= f1;
+    }
+    m = ref = to;
+    limit = to + slack;
+  }
+  __device__ __forceinline__ void add(float2 z, float scale) {
+    const float2 x = __fadd2_rn(z, {-ref, -ref});
+    const float2 d = __fmul2_rn(x, {scale, scale});
+    const float2 e = {exp2_fast(d.x), exp2_fast(d.y)};
+    s = __fadd2_rn(s, e);
+    if (ENTROPY) u = __ffma2_rn(e, {clamped(d.x), clamped(d.y)}, u);
+    if (OWN) {
+      const float2 d1 = __fmul2_rn(x, {kLog2e, kLog2e});
+      s1 = __fadd2_rn(s1, {exp2_fast(d1.x), exp2_fast(d1.y)});
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void add_chunk(const uint32_t* w, float scale, float slack) {
+    const float cm = max_of(w, T());
+    if (cm > limit) move_to(cm, scale, slack);
+#pragma unroll
+    for (int i = 0; i < kPer<T> / 2; ++i) add(pair_of(w, i, T()), scale);
+  }
+  __device__ __forceinline__ void add_one(float z, float scale, float slack) {
+    if (z > limit) move_to(z, scale, slack);
+    add({z, -INFINITY}, scale);
+  }
+};
+
+// What a group of threads knows of a row: m and the sums relative to it
+// (m = -inf: no finite logit, sums 0 or NaN).
+struct Sums {
+  float m, s, u, s1;
+};
+// The factor's exponent from reference m to the group's M.
+__device__ __forceinline__ float toward(float m, float M, float scale) {
+  return M == -INFINITY ? 0.0f : clamped((m - M) * scale);
+}
+__device__ __forceinline__ Sums moved(const Sums& a, float M, float scale) {
+  const float delta = toward(a.m, M, scale), f = exp2_fast(delta);
+  const float f1 = exp2_fast(toward(a.m, M, kLog2e));
+  return {M, f * a.s, f * fmaf(a.s, delta, a.u), f1 * a.s1};
+}
+
+// The block's sums, in a fixed order; every thread gets them.
+template <int THREADS>
+__device__ __forceinline__ Sums block_sums(Sums t, float scale, Sums* sm) {
+  float M = t.m;
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+  t = moved(t, M, scale);
+  for (int off = 16; off > 0; off >>= 1) {
+    t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, off);
+    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
+    t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
+  }
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = t;
+  __syncthreads();
+  M = sm[0].m;
+  for (int w = 1; w < THREADS / 32; ++w) M = fmaxf(M, sm[w].m);
+  Sums all = {M, 0.0f, 0.0f, 0.0f};
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const Sums x = moved(sm[w], M, scale);
+    all.s += x.s;
+    all.u += x.u;
+    all.s1 += x.s1;
+  }
+  return all;
+}
+
+// The sums of a row by one block: each thread keeps kFlight chunks in flight
+// ahead of those that it works on.
+constexpr int kFlight = 2;
+template <typename T, bool ENTROPY, bool OWN>
+__device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float slack, Sums* sm,
+                                         unsigned int* err) {
+  const int tid = threadIdx.x;
+  const Span sp = span_of(z, V);
+  const T* body = z + sp.head;
+  Stats<ENTROPY, OWN> st;
+  uint32_t now[kFlight][kWords], next[kFlight][kWords];
+  auto load = [&](uint32_t(*w)[kWords], int q0) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int q = q0 + f * kThreads + tid;
+      if (q < sp.body && within(sp.head + (int64_t)q * kPer<T>,
+                                sp.head + (int64_t)(q + 1) * kPer<T>, 0, V, err))
+        load_chunk(w[f], body + (int64_t)q * kPer<T>);
+    }
+  };
+  load(now, 0);
+  if (tid < sp.head) st.add_one(value_of(z[tid]), scale, slack);
+  if (tid < sp.tail) st.add_one(value_of(z[V - sp.tail + tid]), scale, slack);
+  for (int q0 = 0; q0 < sp.body; q0 += kFlight * kThreads) {
+    load(next, q0 + kFlight * kThreads);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+      if (q0 + f * kThreads + tid < sp.body)
+        st.template add_chunk<T>(now[f], scale, slack);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
+  }
+  return block_sums<kThreads>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
+                              sm);
+}
 
 template <typename F>
 __device__ __forceinline__ float block_reduce(float x, float* sm, F f) {
@@ -80,13 +270,14 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
 
 // One block per row. LOSS: statistics and losses from the logits; GRAD: the
 // gradient, from them or from the forward call's normalisers.
-template <typename T, bool LOSS, bool GRAD>
+template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
   overlap_wait();
   const int64_t r = blockIdx.x;
   const int V = a.vocab, K = a.teacher_k, tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.logits) + r * a.row_stride;
   __shared__ float sm[kThreads / 32];
+  __shared__ Sums sm_sums[kThreads / 32];
   __shared__ uint64_t sm_key[kThreads / 32];
   __shared__ int32_t s_id[ZS_MAX_TEACHER + 1];
   __shared__ float s_q[ZS_MAX_TEACHER], s_lnq[ZS_MAX_TEACHER], s_z[ZS_MAX_TEACHER + 1];
@@ -142,23 +333,13 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   // Statistics.
   float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f;
   if (LOSS) {
-    float m = -INFINITY;
-    for (int j = tid; j < V; j += kThreads) m = fmaxf(m, value_of(z[j]));
-    m = block_reduce(m, sm, fmax_);
+    const Sums t = row_sums<T, ENTROPY, OWN>(z, V, a.scale, a.slack, sm_sums, a.err);
+    const float m = t.m, U = t.u;
     M = m == -INFINITY ? 0.0f : m;  // a row masked throughout: every e is 2^-inf = 0
-    float s = 0.0f, u = 0.0f, s1 = 0.0f;
-    for (int j = tid; j < V; j += kThreads) {
-      const float x = value_of(z[j]) - M;
-      const float d = x * a.scale, e = exp2f(d);
-      s += e;
-      u = fmaf(e, fmaxf(d, -1e4f), u);  // e is 0 below the clamp, and 0 * -inf is not
-      if (a.hard_own) s1 += exp2f(x * kLog2e);
-    }
-    S = block_reduce(s, sm, fadd_);
-    const float U = block_reduce(u, sm, fadd_);
-    S1 = a.hard_own ? block_reduce(s1, sm, fadd_) : S;
+    S = t.s;
+    S1 = OWN ? t.s1 : S;
     const bool empty = m == -INFINITY && S == 0.0f;
-    const float ln_s = logf(S), ln_s1 = a.hard_own ? logf(S1) : ln_s;
+    const float ln_s = logf(S), ln_s1 = OWN ? logf(S1) : ln_s;
     lse = empty ? -INFINITY : fmaf(M, a.inv_t, ln_s);
     lse1 = empty ? -INFINITY : M + ln_s1;
     if (tid == 0) {
@@ -218,7 +399,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     if (LOSS) {
       zero = lse == -INFINITY;
       A = w * a.inv_t * Q / S;
-      if (a.hard_own)
+      if (OWN)
         A1 = -al / S1;
       else
         A -= al / S;
@@ -230,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       M = lse / a.inv_t;
       M1 = lse1;
       A = w * a.inv_t * Q;
-      if (a.hard_own)
+      if (OWN)
         A1 = -al;
       else
         A -= al;
@@ -279,10 +460,9 @@ RowArgs row_args(const VocabLaunch& in) {
   a.teacher_k = in.teacher_k;
   a.teacher_bf16 = in.teacher_dtype == ZS_BF16;
   a.distill = in.distill;
-  a.hard_own = in.distill && in.temperature != 1.0 &&
-               (in.logprob || in.hard_lse || in.d_logprob);
   a.inv_t = (float)(1.0 / in.temperature);
   a.scale = (float)(1.4426950408889634 / in.temperature);
+  a.slack = (float)(8.0 / 1.4426950408889634 * (in.temperature < 1.0 ? in.temperature : 1.0));
   a.targets = in.targets;
   a.teacher_ids = in.teacher_ids;
   a.teacher_logits = in.teacher_logits;
@@ -304,25 +484,38 @@ RowArgs row_args(const VocabLaunch& in) {
   return a;
 }
 
-template <bool LOSS, bool GRAD>
+template <bool LOSS, bool GRAD, bool ENTROPY, bool OWN>
 cudaError_t launch(const VocabLaunch& in, cudaStream_t stream) {
   const RowArgs a = row_args(in);
   if (!a.err) return cudaErrorInvalidSymbol;
   const dim3 grid((unsigned)in.rows);
   return in.dtype == ZS_BF16
-             ? launch_kernel(rows_kernel<__nv_bfloat16, LOSS, GRAD>, grid, dim3(kThreads), 0,
-                             stream, a)
-             : launch_kernel(rows_kernel<float, LOSS, GRAD>, grid, dim3(kThreads), 0, stream, a);
+             ? launch_kernel(rows_kernel<__nv_bfloat16, LOSS, GRAD, ENTROPY, OWN>, grid,
+                             dim3(kThreads), 0, stream, a)
+             : launch_kernel(rows_kernel<float, LOSS, GRAD, ENTROPY, OWN>, grid, dim3(kThreads),
+                             0, stream, a);
+}
+
+// The hard labels need a softmax of their own: T is not 1, and one of their
+// values is wanted.
+bool own_softmax(const VocabLaunch& a) {
+  return a.distill && a.temperature != 1.0 && (a.logprob || a.hard_lse || a.d_logprob);
 }
 
 }  // namespace
 
 cudaError_t launch_vocab_loss(const VocabLaunch& a, cudaStream_t stream) {
-  return a.d_logits ? launch<true, true>(a, stream) : launch<true, false>(a, stream);
+  if (a.d_logits)
+    return own_softmax(a) ? launch<true, true, false, true>(a, stream)
+                          : launch<true, true, false, false>(a, stream);
+  if (a.entropy) return launch<true, false, true, false>(a, stream);
+  return own_softmax(a) ? launch<true, false, false, true>(a, stream)
+                        : launch<true, false, false, false>(a, stream);
 }
 
 cudaError_t launch_vocab_grad(const VocabLaunch& a, cudaStream_t stream) {
-  return launch<false, true>(a, stream);
+  return own_softmax(a) ? launch<false, true, false, true>(a, stream)
+                        : launch<false, true, false, false>(a, stream);
 }
 
 }  // namespace zs
