@@ -243,6 +243,99 @@ __device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float s
                               sm);
 }
 
+// ---- the gradient's smooth part -------------------------------------------------
+// g_j = 2^d (A + B d) + 2^d1 A1 with d = (z_j - M) scale, d1 = (z_j - M1) log2(e):
+// the row's constants. zero: the whole row's gradient is 0.
+struct GradRow {
+  float A, B, A1, M, M1, scale;
+  bool zero;
+};
+template <bool ENTROPY, bool OWN>
+__device__ __forceinline__ float2 smooth(const GradRow& r, float2 z) {
+  const float2 d = __fmul2_rn(__fadd2_rn(z, {-r.M, -r.M}), {r.scale, r.scale});
+  const float2 e = {exp2_fast(d.x), exp2_fast(d.y)};
+  float2 c = {r.A, r.A};
+  if (ENTROPY) c = __ffma2_rn({r.B, r.B}, {clamped(d.x), clamped(d.y)}, c);
+  float2 g = __fmul2_rn(e, c);
+  if (OWN) {
+    const float2 d1 = __fmul2_rn(__fadd2_rn(z, {-r.M1, -r.M1}), {kLog2e, kLog2e});
+    g = __ffma2_rn({exp2_fast(d1.x), exp2_fast(d1.y)}, {r.A1, r.A1}, g);
+  }
+  return g;
+}
+__device__ __forceinline__ void put_pair(uint32_t* w, int i, float2 g, __nv_bfloat16) {
+  const __nv_bfloat162 b = __float22bfloat162_rn(g);
+  w[i] = *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void put_pair(uint32_t* w, int i, float2 g, float) {
+  w[2 * i] = __float_as_uint(g.x);
+  w[2 * i + 1] = __float_as_uint(g.y);
+}
+__device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Writes the smooth part of a row's gradient. Each element is read and written
+// by one thread, so g may be z. Rows of z and g that sit differently in their
+// 32-byte chunks (other strides or bases) go element by element.
+template <typename T, bool ENTROPY, bool OWN>
+__device__ __forceinline__ void write_row(const T* z, T* g, int V, const GradRow& r,
+                                          unsigned int* err) {
+  const int tid = threadIdx.x;
+  if (((uintptr_t)z ^ (uintptr_t)g) % kChunkBytes != 0) {
+#pragma unroll 4
+    for (int j = tid; j < V; j += kThreads)
+      store(g + j, r.zero ? 0.0f : smooth<ENTROPY, OWN>(r, {value_of(z[j]), 0.0f}).x);
+    return;
+  }
+  const Span sp = span_of(z, V);
+  auto one = [&](int j) {
+    store(g + j, r.zero ? 0.0f : smooth<ENTROPY, OWN>(r, {value_of(z[j]), 0.0f}).x);
+  };
+  if (tid < sp.head) one(tid);
+  if (tid < sp.tail) one(V - sp.tail + tid);
+  const T* zb = z + sp.head;
+  T* gb = g + sp.head;
+  auto in_row = [&](int q) {
+    return q < sp.body && within(sp.head + (int64_t)q * kPer<T>,
+                                 sp.head + (int64_t)(q + 1) * kPer<T>, 0, V, err);
+  };
+  uint32_t now[kFlight][kWords], next[kFlight][kWords], out[kWords];
+  if (r.zero) {  // not read at all: it may hold anything
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) out[i] = 0;
+    for (int q = tid; q < sp.body; q += kThreads)
+      if (in_row(q)) store_chunk(gb + (int64_t)q * kPer<T>, out);
+    return;
+  }
+  auto load = [&](uint32_t(*w)[kWords], int q0) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int q = q0 + f * kThreads + tid;
+      if (in_row(q)) load_chunk(w[f], zb + (int64_t)q * kPer<T>);
+    }
+  };
+  load(now, 0);
+  for (int q0 = 0; q0 < sp.body; q0 += kFlight * kThreads) {
+    load(next, q0 + kFlight * kThreads);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int q = q0 + f * kThreads + tid;
+      if (!in_row(q)) continue;
+#pragma unroll
+      for (int i = 0; i < kPer<T> / 2; ++i)
+        put_pair(out, i, smooth<ENTROPY, OWN>(r, pair_of(now[f], i, T())), T());
+      store_chunk(gb + (int64_t)q * kPer<T>, out);
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
+  }
+}
+
 template <typename F>
 __device__ __forceinline__ float block_reduce(float x, float* sm, F f) {
   for (int off = 16; off > 0; off >>= 1) x = f(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
@@ -390,7 +483,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   }
 
   if (GRAD) {
-    // g_j = e_j (A + B d_j) [+ e1_j A1], e_j = 2^((z_j - M) scale).
     T* g = static_cast<T*>(a.d_logits) + r * a.grad_stride;
     const float al = a.d_logprob && target >= 0 ? a.d_logprob[r] : 0.0f;
     const float w = a.d_loss ? a.d_loss[r] : 0.0f, b = a.d_entropy ? a.d_entropy[r] : 0.0f;
@@ -425,14 +517,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       at_target = al * a.inv_t;
     }
     zero = zero || (al == 0.0f && w == 0.0f && b == 0.0f);
-    auto smooth = [&](float zj) {
-      const float d = (zj - M) * a.scale;
-      float x = 0.0f;
-      if (A != 0.0f || B != 0.0f) x = exp2f(d) * fmaf(B, fmaxf(d, -1e4f), A);
-      if (A1 != 0.0f) x = fmaf(exp2f((zj - M1) * kLog2e), A1, x);
-      return x;
-    };
-    for (int j = tid; j < V; j += kThreads) store(g + j, zero ? 0.0f : smooth(value_of(z[j])));
+    // A softmax without weight must not meet its normaliser (it may belong to
+    // another temperature): infinity turns its exponentials into 0.
+    if (A == 0.0f && B == 0.0f) M = INFINITY;
+    if (A1 == 0.0f) M1 = INFINITY;
+    const GradRow row = {A, B, A1, M, M1, a.scale, zero};
+    write_row<T, ENTROPY, OWN>(z, g, V, row, a.err);
     __syncthreads();
     // The columns of the target and the teacher's ids, from the logits kept
     // above (z may be overwritten by now). Equal ids all store the same value.
@@ -442,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       float q = 0.0f;
       for (int i = 0; i < K; ++i)
         if (s_id[i] == id) q += s_q[i];
-      float x = smooth(s_z[k]) - w * a.inv_t * q;
+      float x = smooth<ENTROPY, OWN>(row, {s_z[k], 0.0f}).x - w * a.inv_t * q;
       if (id == target) x += at_target;
       store(g + id, x);
     }
@@ -514,6 +604,7 @@ cudaError_t launch_vocab_loss(const VocabLaunch& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_vocab_grad(const VocabLaunch& a, cudaStream_t stream) {
+  if (a.d_entropy) return launch<false, true, true, false>(a, stream);
   return own_softmax(a) ? launch<false, true, false, true>(a, stream)
                         : launch<false, true, false, false>(a, stream);
 }

@@ -430,6 +430,17 @@ def test_distill_in_place_and_parts(dtype, mode):
         _check_distill(4, 5003, 0, dtype, mode=mode)   # cross entropy of the targets alone
 
 
+@pytest.mark.parametrize("mode", ["grad", "fused"])
+@pytest.mark.parametrize("T", [0.05, 20.0])
+def test_distill_one_loss_weighted_at_another_temperature(T, mode):
+    """Logits of some hundreds, whose exponentials at the other temperature are
+    out of range."""
+    z = torch.randn(4, 3001, generator=torch.Generator().manual_seed(9)) * 60 + 100
+    for dtype in (BF16, FP32):
+        _check_distill(4, 3001, 5, dtype, T=T, mode=mode, soft=False, z=z)
+        _check_distill(4, 3001, 5, dtype, T=T, mode=mode, hard=False, z=z)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("V", [5, 3000, 20001])
 def test_masked_rows_and_unweighted_rows_have_no_gradient(V, dtype):
