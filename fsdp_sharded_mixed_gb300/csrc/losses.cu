@@ -18,6 +18,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bounds.cuh"
 #include "overlap.cuh"
 #include "zs_internal.h"
@@ -28,6 +30,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 256;
+constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a block
 
 struct RowArgs {
   const void* logits;
@@ -153,11 +156,12 @@ struct Stats {
     }
   }
   template <typename T>
-  __device__ __forceinline__ void add_chunk(const uint32_t* w, float scale, float slack) {
+  __device__ __forceinline__ float add_chunk(const uint32_t* w, float scale, float slack) {
     const float cm = max_of(w, T());
     if (cm > limit) move_to(cm, scale, slack);
 #pragma unroll
     for (int i = 0; i < kPer<T> / 2; ++i) add(pair_of(w, i, T()), scale);
+    return cm;
   }
   __device__ __forceinline__ void add_one(float z, float scale, float slack) {
     if (z > limit) move_to(z, scale, slack);
@@ -205,12 +209,140 @@ __device__ __forceinline__ Sums block_sums(Sums t, float scale, Sums* sm) {
   return all;
 }
 
+// ---- the top alternatives -------------------------------------------------------
+// Unique keys that order logits as the alternatives are ranked: NaN above all,
+// then by value (-0 as +0), then the lowest position first. 0 is below them all.
+// The value takes the upper half; of a bf16's only the upper 16 bits count.
+template <typename T>
+__device__ __forceinline__ uint64_t rank_key(float z, int32_t position) {
+  uint32_t u = __float_as_uint(z + 0.0f);
+  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  if (z != z) u = 0xFFFFFFFFu;
+  if (sizeof(T) == 2) u &= 0xFFFF0000u;
+  return ((uint64_t)u << 32) | (uint32_t)~position;
+}
+
+// The pass over the row leaves every chunk's maximum in shared memory, and each
+// thread knows the best of its own chunks. A chunk is ranked by its maximum,
+// equal ones by position. If k chunks reach a bound, the row's top k elements
+// do, each taken at its chunk's position: an element below the bound is beaten
+// by the maxima of all k. So a bound that about k of the threads' best chunks
+// reach leaves few chunks to read again and few elements to rank.
+// Table entry p: body chunk p; then the tail and the head (whose position comes
+// first). An end without elements has key 0. Entry p belongs to thread p modulo
+// the block.
+constexpr int kListed = 2048;  // elements that are ranked; 16 * ZS_MAX_TOP at least
+struct TopShared {
+  uint64_t list[kListed];
+  uint64_t best[ZS_MAX_TOP];
+  int count, total;
+};
+// A bound that at least k of the keys reach, and at most `most` where unique
+// keys allow it: bit by bit from the top, count(bound) being how many keys of
+// the block are >= bound (called by all its threads).
+template <typename T, typename F>
+__device__ __forceinline__ uint64_t bound_of(int k, int most, F count) {
+  uint64_t bound = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    if (sizeof(T) == 2 && bit >= 32 && bit < 48) continue;  // 0 in every key
+    const uint64_t tried = bound | (uint64_t(1) << bit);
+    const int n = count(tried);
+    if (n < k) continue;
+    bound = tried;
+    if (n <= most) break;
+  }
+  return bound;
+}
+
+template <typename T>
+struct Chunks {  // the table of a row
+  Span sp;
+  int V;
+  const T* maxima;
+  __device__ __forceinline__ int count() const { return sp.body + 2; }
+  __device__ __forceinline__ int position(int p) const { return p == sp.body + 1 ? 0 : p + 1; }
+  __device__ __forceinline__ uint64_t key(int p) const {
+    if ((p == sp.body && sp.tail == 0) || (p == sp.body + 1 && sp.head == 0)) return 0;
+    return rank_key<T>(value_of(maxima[p]), position(p));
+  }
+  __device__ __forceinline__ void elements(int p, int* lo, int* hi) const {
+    *lo = p == sp.body + 1 ? 0 : sp.head + p * kPer<T>;
+    *hi = p == sp.body + 1 ? sp.head : min(V, *lo + kPer<T>);
+  }
+};
+
+// Ranks the row's top k into sh.best (keys, best first; position = column).
+// `mine`: the best key of the thread's body chunks.
+template <typename T, int THREADS>
+__device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int k, uint64_t mine,
+                                           TopShared& sh, unsigned int* err) {
+  const int tid = threadIdx.x;
+  for (int p = ch.sp.body; p < ch.count(); ++p)
+    if (p % THREADS == tid) mine = max(mine, ch.key(p));
+  auto total_of = [&](int n) {
+    __syncthreads();
+    if (tid == 0) sh.total = 0;
+    __syncthreads();
+    if (n) atomicAdd(&sh.total, n);
+    __syncthreads();
+    return sh.total;
+  };
+  // Lists the elements at or above the bound, from the chunks that reach it.
+  auto list_from = [&](uint64_t bound, bool look) {
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    for (int p = tid; look && p < ch.count(); p += THREADS) {
+      if (ch.key(p) < bound || ch.key(p) == 0) continue;
+      int lo, hi;
+      ch.elements(p, &lo, &hi);
+      for (int j = lo; j < hi; ++j) {
+        if (!within(j, j + 1, 0, ch.V, err)) continue;
+        const float x = value_of(z[j]);
+        if (rank_key<T>(x, ch.position(p)) < bound) continue;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kListed) sh.list[at] = rank_key<T>(x, j);
+      }
+    }
+    __syncthreads();
+    return sh.count;
+  };
+  uint64_t bound =
+      bound_of<T>(k, 2 * k, [&](uint64_t b) { return __syncthreads_count(mine >= b); });
+  int n = list_from(bound, mine >= bound);
+  if (n > kListed) {
+    // Very many in a few threads' chunks: the exact k-th best chunk leaves the
+    // elements of k chunks at most.
+    bound = bound_of<T>(k, k, [&](uint64_t b) {
+      int reach = 0;
+      for (int p = tid; p < ch.count(); p += THREADS) reach += ch.key(p) >= b;
+      return total_of(reach);
+    });
+    n = list_from(bound, true);
+  }
+  bound = 0;
+  if (n > kListed / 4)  // ranking is quadratic: first the exact k-th best
+    bound = bound_of<T>(k, k, [&](uint64_t b) {
+      int reach = 0;
+      for (int i = tid; i < n; i += THREADS) reach += sh.list[i] >= b;
+      return total_of(reach);
+    });
+  // The list's order is that of its atomics; the ranks are not.
+  for (int i = tid; i < n; i += THREADS) {
+    const uint64_t key = sh.list[i];
+    if (key < bound) continue;
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sh.list[j] > key;
+    if (rank < k) sh.best[rank] = key;
+  }
+  __syncthreads();
+}
+
 // The sums of a row by one block: each thread keeps kFlight chunks in flight
-// ahead of those that it works on.
+// ahead of those that it works on. TOP: maxima and the thread's best chunk.
 constexpr int kFlight = 2;
-template <typename T, bool ENTROPY, bool OWN>
+template <typename T, bool ENTROPY, bool OWN, bool TOP>
 __device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float slack, Sums* sm,
-                                         unsigned int* err) {
+                                         T* maxima, uint64_t* best, unsigned int* err) {
   const int tid = threadIdx.x;
   const Span sp = span_of(z, V);
   const T* body = z + sp.head;
@@ -228,12 +360,30 @@ __device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float s
   load(now, 0);
   if (tid < sp.head) st.add_one(value_of(z[tid]), scale, slack);
   if (tid < sp.tail) st.add_one(value_of(z[V - sp.tail + tid]), scale, slack);
+  if (TOP && tid < 32) {
+    float h = tid < sp.head ? value_of(z[tid]) : -INFINITY;
+    float t = tid < sp.tail ? value_of(z[V - sp.tail + tid]) : -INFINITY;
+    for (int off = 16; off > 0; off >>= 1) {
+      h = max_nan(h, __shfl_xor_sync(0xFFFFFFFFu, h, off));
+      t = max_nan(t, __shfl_xor_sync(0xFFFFFFFFu, t, off));
+    }
+    if (tid == 0) {
+      store(maxima + sp.body, t);
+      store(maxima + sp.body + 1, h);
+    }
+  }
   for (int q0 = 0; q0 < sp.body; q0 += kFlight * kThreads) {
     load(next, q0 + kFlight * kThreads);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (q0 + f * kThreads + tid < sp.body)
-        st.template add_chunk<T>(now[f], scale, slack);
+      if (q0 + f * kThreads + tid < sp.body) {
+        const float cm = st.template add_chunk<T>(now[f], scale, slack);
+        if (TOP) {
+          const int p = q0 + f * kThreads + tid;
+          store(maxima + p, cm);
+          *best = max(*best, rank_key<T>(cm, p + 1));
+        }
+      }
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
 #pragma unroll
@@ -347,15 +497,6 @@ __device__ __forceinline__ float block_reduce(float x, float* sm, F f) {
   return x;
 }
 
-// Unique keys that order logits as the alternatives are ranked: NaN above all,
-// then by value (-0 as +0), then the lowest column first.
-__device__ __forceinline__ uint64_t rank_key(float z, int32_t column) {
-  uint32_t u = __float_as_uint(z + 0.0f);
-  u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-  if (z != z) u = 0xFFFFFFFFu;
-  return ((uint64_t)u << 32) | (uint32_t)~column;
-}
-
 __device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
   return a.teacher_bf16 ? value_of(static_cast<const __nv_bfloat16*>(a.teacher_logits)[i])
                         : static_cast<const float*>(a.teacher_logits)[i];
@@ -363,7 +504,7 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
 
 // One block per row. LOSS: statistics and losses from the logits; GRAD: the
 // gradient, from them or from the forward call's normalisers.
-template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN>
+template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
   overlap_wait();
   const int64_t r = blockIdx.x;
@@ -371,7 +512,6 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   const T* z = static_cast<const T*>(a.logits) + r * a.row_stride;
   __shared__ float sm[kThreads / 32];
   __shared__ Sums sm_sums[kThreads / 32];
-  __shared__ uint64_t sm_key[kThreads / 32];
   __shared__ int32_t s_id[ZS_MAX_TEACHER + 1];
   __shared__ float s_q[ZS_MAX_TEACHER], s_lnq[ZS_MAX_TEACHER], s_z[ZS_MAX_TEACHER + 1];
   auto fmax_ = [](float x, float y) { return fmaxf(x, y); };
@@ -426,7 +566,12 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
   // Statistics.
   float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f;
   if (LOSS) {
-    const Sums t = row_sums<T, ENTROPY, OWN>(z, V, a.scale, a.slack, sm_sums, a.err);
+    extern __shared__ __align__(16) unsigned char dynamic[];
+    TopShared* top = reinterpret_cast<TopShared*>(dynamic);
+    T* maxima = reinterpret_cast<T*>(top + 1);
+    uint64_t best = 0;
+    const Sums t = row_sums<T, ENTROPY, OWN, TOP>(z, V, a.scale, a.slack, sm_sums, maxima, &best,
+                                                  a.err);
     const float m = t.m, U = t.u;
     M = m == -INFINITY ? 0.0f : m;  // a row masked throughout: every e is 2^-inf = 0
     S = t.s;
@@ -454,27 +599,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
       l = block_reduce(l, sm, fadd_);
       if (tid == 0) a.loss[r] = l;
     }
-    // The alternatives: the largest key below the last one, top_k times.
-    uint64_t last = ~0ull;
-    for (int k = 0; k < a.top_k; ++k) {
-      uint64_t best = 0;
-      for (int j = tid; j < V; j += kThreads) {
-        const uint64_t key = rank_key(value_of(z[j]), j);
-        if (key < last && key > best) best = key;
-      }
-      for (int off = 16; off > 0; off >>= 1) {
-        const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, best, off);
-        if (o > best) best = o;
-      }
-      __syncthreads();
-      if ((tid & 31) == 0) sm_key[tid >> 5] = best;
-      __syncthreads();
-      best = sm_key[0];
-      for (int w = 1; w < kThreads / 32; ++w)
-        if (sm_key[w] > best) best = sm_key[w];
-      last = best;
-      if (tid == 0) {
-        const int32_t id = (int32_t)~(uint32_t)best;
+    if (TOP) {
+      // block_sums waited for the table
+      select_top<T, kThreads>(z, {span_of(z, V), V, maxima}, a.top_k, best, *top, a.err);
+      for (int k = tid; k < a.top_k; k += kThreads) {
+        const int32_t id = (int32_t)~(uint32_t)top->best[k];
         a.top_ids[r * a.top_k + k] = id;
         a.top_logprobs[r * a.top_k + k] =
             empty ? -INFINITY : (value_of(z[id]) - M) * a.inv_t - ln_s;
@@ -574,16 +703,33 @@ RowArgs row_args(const VocabLaunch& in) {
   return a;
 }
 
-template <bool LOSS, bool GRAD, bool ENTROPY, bool OWN>
-cudaError_t launch(const VocabLaunch& in, cudaStream_t stream) {
+template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
+cudaError_t launch_rows(const VocabLaunch& in, cudaStream_t stream) {
   const RowArgs a = row_args(in);
   if (!a.err) return cudaErrorInvalidSymbol;
-  const dim3 grid((unsigned)in.rows);
+  const auto kernel = rows_kernel<T, LOSS, GRAD, ENTROPY, OWN, TOP>;
+  size_t smem = 0;
+  if (TOP) {
+    // A row's table has an entry for each 32 bytes of its logits and two ends.
+    smem = sizeof(TopShared) + (in.vocab / kPer<T> + 3) * sizeof(T);
+    static std::atomic<bool> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!allowed[dev & 63].load(std::memory_order_acquire)) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+      if (e != cudaSuccess) return e;
+      allowed[dev & 63].store(true, std::memory_order_release);
+    }
+  }
+  return launch_kernel(kernel, dim3((unsigned)in.rows), dim3(kThreads), smem, stream, a);
+}
+
+template <bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
+cudaError_t launch(const VocabLaunch& in, cudaStream_t stream) {
   return in.dtype == ZS_BF16
-             ? launch_kernel(rows_kernel<__nv_bfloat16, LOSS, GRAD, ENTROPY, OWN>, grid,
-                             dim3(kThreads), 0, stream, a)
-             : launch_kernel(rows_kernel<float, LOSS, GRAD, ENTROPY, OWN>, grid, dim3(kThreads),
-                             0, stream, a);
+             ? launch_rows<__nv_bfloat16, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream)
+             : launch_rows<float, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream);
 }
 
 // The hard labels need a softmax of their own: T is not 1, and one of their
@@ -596,17 +742,18 @@ bool own_softmax(const VocabLaunch& a) {
 
 cudaError_t launch_vocab_loss(const VocabLaunch& a, cudaStream_t stream) {
   if (a.d_logits)
-    return own_softmax(a) ? launch<true, true, false, true>(a, stream)
-                          : launch<true, true, false, false>(a, stream);
-  if (a.entropy) return launch<true, false, true, false>(a, stream);
-  return own_softmax(a) ? launch<true, false, false, true>(a, stream)
-                        : launch<true, false, false, false>(a, stream);
+    return own_softmax(a) ? launch<true, true, false, true, false>(a, stream)
+                          : launch<true, true, false, false, false>(a, stream);
+  if (a.top_k) return launch<true, false, true, false, true>(a, stream);
+  if (a.entropy) return launch<true, false, true, false, false>(a, stream);
+  return own_softmax(a) ? launch<true, false, false, true, false>(a, stream)
+                        : launch<true, false, false, false, false>(a, stream);
 }
 
 cudaError_t launch_vocab_grad(const VocabLaunch& a, cudaStream_t stream) {
-  if (a.d_entropy) return launch<false, true, true, false>(a, stream);
-  return own_softmax(a) ? launch<false, true, false, true>(a, stream)
-                        : launch<false, true, false, false>(a, stream);
+  if (a.d_entropy) return launch<false, true, true, false, false>(a, stream);
+  return own_softmax(a) ? launch<false, true, false, true, false>(a, stream)
+                        : launch<false, true, false, false, false>(a, stream);
 }
 
 }  // namespace zs
