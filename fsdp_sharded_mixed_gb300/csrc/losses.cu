@@ -29,14 +29,20 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kThreads = 256;
-constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a block
+constexpr int kLong = 256, kShort = 32;  // threads of a row's block
+constexpr int kResident = 1024;          // threads of an SM: 64 registers each
+constexpr int kSMs = 152;
+constexpr int kMaxSplit = 8;               // blocks of a row: the portable cluster size
+constexpr int kShortChunks = 256;         // rows up to this many go to one warp each
+constexpr int64_t kRowsInL2 = 64 << 20;   // bytes of rows in flight that L2 (129 MB) keeps
+constexpr int64_t kTableBytes = 40 << 10;
+constexpr int kMaxSmem = 200 * 1024;      // dynamic shared memory of a block
 
 struct RowArgs {
   const void* logits;
   void* d_logits;
   int64_t row_stride, grad_stride;
-  int32_t vocab, top_k, teacher_k;
+  int32_t vocab, shift, top_k, teacher_k;  // a row has 2^shift blocks
   bool teacher_bf16;
   bool distill;   // targets are hard labels at T = 1
   float inv_t, scale, slack;  // 1/T, log2(e)/T, how far logits may exceed a reference
@@ -64,14 +70,26 @@ constexpr int kWords = kChunkBytes / 4;
 template <typename T>
 constexpr int kPer = kChunkBytes / (int)sizeof(T);
 
-struct Span {
+// A block's part of a row: part `rank` of 2^shift takes its share of the body;
+// the first one the head as well, the last one the tail.
+struct Part {
+  int lo, hi;            // its elements
   int head, body, tail;  // elements, chunks, elements
+  int chunk0;            // its first chunk's place in the whole row's body
 };
 template <typename T>
-__device__ __forceinline__ Span span_of(const T* z, int V) {
+__device__ __forceinline__ Part part_of(const T* z, int V, int rank, int shift) {
   const int head = min(V, (int)((0 - (uintptr_t)z) % kChunkBytes / sizeof(T)));
   const int body = (V - head) / kPer<T>;
-  return {head, body, V - head - body * kPer<T>};
+  const int c0 = body * rank >> shift, c1 = body * (rank + 1) >> shift;  // below 2^21
+  Part p;
+  p.chunk0 = c0;
+  p.body = c1 - c0;
+  p.head = rank == 0 ? head : 0;
+  p.lo = rank == 0 ? 0 : head + c0 * kPer<T>;
+  p.tail = rank + 1 == 1 << shift ? V - head - body * kPer<T> : 0;
+  p.hi = head + c1 * kPer<T> + p.tail;
+  return p;
 }
 
 __device__ __forceinline__ void load_chunk(uint32_t* w, const void* p) {
@@ -184,24 +202,39 @@ __device__ __forceinline__ Sums moved(const Sums& a, float M, float scale) {
   return {M, f * a.s, f * fmaf(a.s, delta, a.u), f1 * a.s1};
 }
 
-// The block's sums, in a fixed order; every thread gets them.
+// The block's sums, in a fixed order, and the largest of its u; every thread
+// gets them.
+struct BlockSums {
+  Sums sums[kLong / 32];
+  float u[kLong / 32];
+};
 template <int THREADS>
-__device__ __forceinline__ Sums block_sums(Sums t, float scale, Sums* sm) {
+__device__ __forceinline__ Sums block_sums(Sums t, float scale, float* u, BlockSums& sm) {
   float M = t.m;
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+  for (int off = 16; off > 0; off >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    *u = fmaxf(*u, __shfl_xor_sync(0xFFFFFFFFu, *u, off));
+  }
   t = moved(t, M, scale);
   for (int off = 16; off > 0; off >>= 1) {
     t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, off);
     t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
     t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
   }
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = t;
+  if ((threadIdx.x & 31) == 0) {
+    sm.sums[threadIdx.x >> 5] = t;
+    sm.u[threadIdx.x >> 5] = *u;
+  }
   __syncthreads();
-  M = sm[0].m;
-  for (int w = 1; w < THREADS / 32; ++w) M = fmaxf(M, sm[w].m);
+  if (THREADS == 32) return t;
+  M = sm.sums[0].m;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    M = fmaxf(M, sm.sums[w].m);
+    *u = fmaxf(*u, sm.u[w]);
+  }
   Sums all = {M, 0.0f, 0.0f, 0.0f};
   for (int w = 0; w < THREADS / 32; ++w) {
-    const Sums x = moved(sm[w], M, scale);
+    const Sums x = moved(sm.sums[w], M, scale);
     all.s += x.s;
     all.u += x.u;
     all.s1 += x.s1;
@@ -222,6 +255,13 @@ __device__ __forceinline__ uint64_t rank_key(float z, int32_t position) {
   return ((uint64_t)u << 32) | (uint32_t)~position;
 }
 
+template <typename T>
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  const uint32_t bits = (u & 0x80000000u) ? u ^ 0x80000000u : ~u;
+  return __uint_as_float(sizeof(T) == 2 ? bits & 0xFFFF0000u : bits);
+}
+
 // The pass over the row leaves every chunk's maximum in shared memory, and each
 // thread knows the best of its own chunks. A chunk is ranked by its maximum,
 // equal ones by position. If k chunks reach a bound, the row's top k elements
@@ -232,10 +272,13 @@ __device__ __forceinline__ uint64_t rank_key(float z, int32_t position) {
 // first). An end without elements has key 0. Entry p belongs to thread p modulo
 // the block.
 constexpr int kListed = 2048;  // elements that are ranked; 16 * ZS_MAX_TOP at least
+constexpr int kFound = 512;    // chunks that are read again; ZS_MAX_TOP at least
 struct TopShared {
-  uint64_t list[kListed];
   uint64_t best[ZS_MAX_TOP];
+  int found[kFound];
   int count, total;
+  int capacity;    // of the list: kListed, or the whole of a shorter row
+  uint64_t* list;  // after this, then the table
 };
 // A bound that at least k of the keys reach, and at most `most` where unique
 // keys allow it: bit by bit from the top, count(bound) being how many keys of
@@ -255,23 +298,25 @@ __device__ __forceinline__ uint64_t bound_of(int k, int most, F count) {
 }
 
 template <typename T>
-struct Chunks {  // the table of a row
-  Span sp;
-  int V;
+struct Chunks {  // the table of a block's part
+  Part sp;
   const T* maxima;
   __device__ __forceinline__ int count() const { return sp.body + 2; }
-  __device__ __forceinline__ int position(int p) const { return p == sp.body + 1 ? 0 : p + 1; }
+  __device__ __forceinline__ int position(int p) const {
+    return p == sp.body + 1 ? 0 : sp.chunk0 + p + 1;
+  }
   __device__ __forceinline__ uint64_t key(int p) const {
     if ((p == sp.body && sp.tail == 0) || (p == sp.body + 1 && sp.head == 0)) return 0;
     return rank_key<T>(value_of(maxima[p]), position(p));
   }
   __device__ __forceinline__ void elements(int p, int* lo, int* hi) const {
-    *lo = p == sp.body + 1 ? 0 : sp.head + p * kPer<T>;
-    *hi = p == sp.body + 1 ? sp.head : min(V, *lo + kPer<T>);
+    *lo = p == sp.body + 1 ? 0 : sp.lo + sp.head + p * kPer<T>;
+    *hi = p == sp.body + 1 ? sp.head : min(sp.hi, *lo + kPer<T>);
   }
 };
 
-// Ranks the row's top k into sh.best (keys, best first; position = column).
+// Ranks the part's top k into sh.best (keys, best first; position = column; 0
+// where the part has no more).
 // `mine`: the best key of the thread's body chunks.
 template <typename T, int THREADS>
 __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int k, uint64_t mine,
@@ -279,6 +324,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
   const int tid = threadIdx.x;
   for (int p = ch.sp.body; p < ch.count(); ++p)
     if (p % THREADS == tid) mine = max(mine, ch.key(p));
+  for (int i = tid; i < k; i += THREADS) sh.best[i] = 0;
   auto total_of = [&](int n) {
     __syncthreads();
     if (tid == 0) sh.total = 0;
@@ -287,21 +333,51 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     __syncthreads();
     return sh.total;
   };
-  // Lists the elements at or above the bound, from the chunks that reach it.
+  // Lists the elements at or above the bound: first the chunks that reach it,
+  // then one thread reads each of them again, so that all their loads are in
+  // flight together. More than fit are counted, not listed.
   auto list_from = [&](uint64_t bound, bool look) {
-    if (tid == 0) sh.count = 0;
+    if (tid == 0) sh.count = sh.total = 0;
     __syncthreads();
+    const float at_least = key_value<T>(bound);
     for (int p = tid; look && p < ch.count(); p += THREADS) {
-      if (ch.key(p) < bound || ch.key(p) == 0) continue;
+      if (value_of(ch.maxima[p]) < at_least) continue;
+      const uint64_t key = ch.key(p);
+      if (key < bound || key == 0) continue;
+      const int at = atomicAdd(&sh.total, 1);
+      if (at < kFound) sh.found[at] = p;
+    }
+    __syncthreads();
+    if (sh.total > kFound) return sh.capacity + 1;
+    for (int f = tid; f < sh.total; f += THREADS) {
+      const int p = sh.found[f];
       int lo, hi;
       ch.elements(p, &lo, &hi);
-      for (int j = lo; j < hi; ++j) {
-        if (!within(j, j + 1, 0, ch.V, err)) continue;
-        const float x = value_of(z[j]);
-        if (rank_key<T>(x, ch.position(p)) < bound) continue;
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kListed) sh.list[at] = rank_key<T>(x, j);
+      if (!within(lo, hi, ch.sp.lo, ch.sp.hi, err)) continue;
+      float x[kPer<T>];
+      if (p < ch.sp.body) {
+        uint32_t w[kWords];
+        load_chunk(w, z + lo);
+#pragma unroll
+        for (int i = 0; i < kPer<T> / 2; ++i) {
+          x[2 * i] = pair_of(w, i, T()).x;
+          x[2 * i + 1] = pair_of(w, i, T()).y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPer<T>; ++i) x[i] = lo + i < hi ? value_of(z[lo + i]) : 0.0f;
       }
+      uint32_t reach = 0;
+#pragma unroll
+      for (int i = 0; i < kPer<T>; ++i)
+        if (lo + i < hi && rank_key<T>(x[i], ch.position(p)) >= bound) reach |= 1u << i;
+      int at = atomicAdd(&sh.count, __popc(reach));
+#pragma unroll
+      for (int i = 0; i < kPer<T>; ++i)
+        if (reach >> i & 1) {
+          if (at < sh.capacity) sh.list[at] = rank_key<T>(x[i], lo + i);
+          ++at;
+        }
     }
     __syncthreads();
     return sh.count;
@@ -309,7 +385,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
   uint64_t bound =
       bound_of<T>(k, 2 * k, [&](uint64_t b) { return __syncthreads_count(mine >= b); });
   int n = list_from(bound, mine >= bound);
-  if (n > kListed) {
+  if (n > sh.capacity) {
     // Very many in a few threads' chunks: the exact k-th best chunk leaves the
     // elements of k chunks at most.
     bound = bound_of<T>(k, k, [&](uint64_t b) {
@@ -337,32 +413,36 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
   __syncthreads();
 }
 
-// The sums of a row by one block: each thread keeps kFlight chunks in flight
-// ahead of those that it works on. TOP: maxima and the thread's best chunk.
+// The sums of a block's part of a row: each thread keeps kFlight chunks in
+// flight ahead of those that it works on. TOP: the table, and the thread's best
+// chunk.
 constexpr int kFlight = 2;
-template <typename T, bool ENTROPY, bool OWN, bool TOP>
-__device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float slack, Sums* sm,
-                                         T* maxima, uint64_t* best, unsigned int* err) {
+// between(): run while the first chunks are on their way; gives u.
+template <typename T, int THREADS, bool ENTROPY, bool OWN, bool TOP, typename F>
+__device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scale, float slack,
+                                          float* u, BlockSums& sm, T* maxima, uint64_t* best,
+                                          unsigned int* err, F between) {
   const int tid = threadIdx.x;
-  const Span sp = span_of(z, V);
-  const T* body = z + sp.head;
+  const T* body = z + sp.lo + sp.head;
   Stats<ENTROPY, OWN> st;
   uint32_t now[kFlight][kWords], next[kFlight][kWords];
   auto load = [&](uint32_t(*w)[kWords], int q0) {
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int q = q0 + f * kThreads + tid;
-      if (q < sp.body && within(sp.head + (int64_t)q * kPer<T>,
-                                sp.head + (int64_t)(q + 1) * kPer<T>, 0, V, err))
-        load_chunk(w[f], body + (int64_t)q * kPer<T>);
+      const int q = q0 + f * THREADS + tid;
+      const int64_t at = (int64_t)q * kPer<T>;
+      if (q < sp.body && within(sp.lo + sp.head + at, sp.lo + sp.head + at + kPer<T>, sp.lo,
+                                sp.hi, err))
+        load_chunk(w[f], body + at);
     }
   };
   load(now, 0);
+  between();
   if (tid < sp.head) st.add_one(value_of(z[tid]), scale, slack);
-  if (tid < sp.tail) st.add_one(value_of(z[V - sp.tail + tid]), scale, slack);
+  if (tid < sp.tail) st.add_one(value_of(z[sp.hi - sp.tail + tid]), scale, slack);
   if (TOP && tid < 32) {
     float h = tid < sp.head ? value_of(z[tid]) : -INFINITY;
-    float t = tid < sp.tail ? value_of(z[V - sp.tail + tid]) : -INFINITY;
+    float t = tid < sp.tail ? value_of(z[sp.hi - sp.tail + tid]) : -INFINITY;
     for (int off = 16; off > 0; off >>= 1) {
       h = max_nan(h, __shfl_xor_sync(0xFFFFFFFFu, h, off));
       t = max_nan(t, __shfl_xor_sync(0xFFFFFFFFu, t, off));
@@ -372,16 +452,16 @@ __device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float s
       store(maxima + sp.body + 1, h);
     }
   }
-  for (int q0 = 0; q0 < sp.body; q0 += kFlight * kThreads) {
-    load(next, q0 + kFlight * kThreads);
+  for (int q0 = 0; q0 < sp.body; q0 += kFlight * THREADS) {
+    load(next, q0 + kFlight * THREADS);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
-      if (q0 + f * kThreads + tid < sp.body) {
+      if (q0 + f * THREADS + tid < sp.body) {
         const float cm = st.template add_chunk<T>(now[f], scale, slack);
         if (TOP) {
-          const int p = q0 + f * kThreads + tid;
+          const int p = q0 + f * THREADS + tid;
           store(maxima + p, cm);
-          *best = max(*best, rank_key<T>(cm, p + 1));
+          *best = max(*best, rank_key<T>(cm, sp.chunk0 + p + 1));
         }
       }
 #pragma unroll
@@ -389,8 +469,85 @@ __device__ __forceinline__ Sums row_sums(const T* z, int V, float scale, float s
 #pragma unroll
       for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
   }
-  return block_sums<kThreads>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
-                              sm);
+  return block_sums<THREADS>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
+                             u, sm);
+}
+
+// ---- the blocks of a row ----------------------------------------------------------
+// A row split over a cluster: each block's sums and best keys, read by the
+// others through the cluster's shared memory.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(at)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ Sums remote_sums(const Sums* p, int rank) {
+  Sums x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.m), "=f"(x.s), "=f"(x.u), "=f"(x.s1)
+               : "r"(remote(p, rank))
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ uint64_t remote_key(const uint64_t* p, int rank) {
+  uint64_t x;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(remote(p, rank)) : "memory");
+  return x;
+}
+
+// The row's sums from its blocks': lane i of every warp reads block i's, and
+// each warp adds them in the same order.
+__device__ __forceinline__ Sums cluster_sums(const Sums* mine, int split, float scale) {
+  const int lane = threadIdx.x & 31;
+  Sums t = remote_sums(mine, lane & (split - 1));
+  float M = t.m;
+  for (int off = 1; off < split; off *= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+  t = moved(t, M, scale);
+  for (int off = 1; off < split; off *= 2) {
+    t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, off);
+    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
+    t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
+  }
+  return t;
+}
+
+// The row's top k from its blocks' sorted lists, into sh.best of this block: a
+// key's rank is its place in its own list plus, for each other list, the number
+// of keys there above it (a binary search in each, all at once).
+template <int THREADS>
+__device__ __forceinline__ void cluster_top(TopShared& sh, int k, int split) {
+  const int tid = threadIdx.x;
+  static_assert(kMaxSplit * 32 <= kLong, "a warp for each block's list");
+  const int own = tid >> 5, lane = tid & 31;
+  if (own < split)
+    for (int i = lane; i < k; i += 32) sh.list[own * k + i] = remote_key(sh.best + i, own);
+  __syncthreads();
+  if (own < split) {
+    for (int i = lane; i < k; i += 32) {
+      const uint64_t key = sh.list[own * k + i];
+      int above[kMaxSplit] = {};
+      for (int step = 128; step > 0; step /= 2) {
+#pragma unroll
+        for (int l = 0; l < kMaxSplit; ++l) {
+          const int at = above[l] + step;
+          if (l < split && at <= k && sh.list[l * k + at - 1] > key) above[l] = at;
+        }
+      }
+      int rank = 0;  // (its own list's part is its place there)
+#pragma unroll
+      for (int l = 0; l < kMaxSplit; ++l) rank += above[l];
+      if (key != 0 && rank < k) sh.best[rank] = key;
+    }
+  }
+  __syncthreads();
 }
 
 // ---- the gradient's smooth part -------------------------------------------------
@@ -427,52 +584,51 @@ __device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// Writes the smooth part of a row's gradient. Each element is read and written
+// Writes the smooth part of the gradient of a block's part of a row. Each element is read and written
 // by one thread, so g may be z. Rows of z and g that sit differently in their
 // 32-byte chunks (other strides or bases) go element by element.
-template <typename T, bool ENTROPY, bool OWN>
-__device__ __forceinline__ void write_row(const T* z, T* g, int V, const GradRow& r,
-                                          unsigned int* err) {
+template <typename T, int THREADS, bool ENTROPY, bool OWN>
+__device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, const GradRow& r,
+                                           unsigned int* err) {
   const int tid = threadIdx.x;
   if (((uintptr_t)z ^ (uintptr_t)g) % kChunkBytes != 0) {
 #pragma unroll 4
-    for (int j = tid; j < V; j += kThreads)
+    for (int j = sp.lo + tid; j < sp.hi; j += THREADS)
       store(g + j, r.zero ? 0.0f : smooth<ENTROPY, OWN>(r, {value_of(z[j]), 0.0f}).x);
     return;
   }
-  const Span sp = span_of(z, V);
   auto one = [&](int j) {
     store(g + j, r.zero ? 0.0f : smooth<ENTROPY, OWN>(r, {value_of(z[j]), 0.0f}).x);
   };
   if (tid < sp.head) one(tid);
-  if (tid < sp.tail) one(V - sp.tail + tid);
-  const T* zb = z + sp.head;
-  T* gb = g + sp.head;
+  if (tid < sp.tail) one(sp.hi - sp.tail + tid);
+  const T* zb = z + sp.lo + sp.head;
+  T* gb = g + sp.lo + sp.head;
   auto in_row = [&](int q) {
-    return q < sp.body && within(sp.head + (int64_t)q * kPer<T>,
-                                 sp.head + (int64_t)(q + 1) * kPer<T>, 0, V, err);
+    const int64_t at = sp.lo + sp.head + (int64_t)q * kPer<T>;
+    return q < sp.body && within(at, at + kPer<T>, sp.lo, sp.hi, err);
   };
   uint32_t now[kFlight][kWords], next[kFlight][kWords], out[kWords];
   if (r.zero) {  // not read at all: it may hold anything
 #pragma unroll
     for (int i = 0; i < kWords; ++i) out[i] = 0;
-    for (int q = tid; q < sp.body; q += kThreads)
+    for (int q = tid; q < sp.body; q += THREADS)
       if (in_row(q)) store_chunk(gb + (int64_t)q * kPer<T>, out);
     return;
   }
   auto load = [&](uint32_t(*w)[kWords], int q0) {
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int q = q0 + f * kThreads + tid;
+      const int q = q0 + f * THREADS + tid;
       if (in_row(q)) load_chunk(w[f], zb + (int64_t)q * kPer<T>);
     }
   };
   load(now, 0);
-  for (int q0 = 0; q0 < sp.body; q0 += kFlight * kThreads) {
-    load(next, q0 + kFlight * kThreads);
+  for (int q0 = 0; q0 < sp.body; q0 += kFlight * THREADS) {
+    load(next, q0 + kFlight * THREADS);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int q = q0 + f * kThreads + tid;
+      const int q = q0 + f * THREADS + tid;
       if (!in_row(q)) continue;
 #pragma unroll
       for (int i = 0; i < kPer<T> / 2; ++i)
@@ -486,15 +642,22 @@ __device__ __forceinline__ void write_row(const T* z, T* g, int V, const GradRow
   }
 }
 
-template <typename F>
-__device__ __forceinline__ float block_reduce(float x, float* sm, F f) {
-  for (int off = 16; off > 0; off >>= 1) x = f(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+// The block's sums of x and y (and of u's largest); every thread gets them.
+template <int THREADS>
+__device__ __forceinline__ float2 block_add(float x, float y, float2* sm) {
+  for (int off = 16; off > 0; off >>= 1) {
+    x += __shfl_xor_sync(0xFFFFFFFFu, x, off);
+    y += __shfl_xor_sync(0xFFFFFFFFu, y, off);
+  }
+  if (THREADS == 32) return {x, y};
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = {x, y};
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sm[0];
-  for (int w = 1; w < kThreads / 32; ++w) x = f(x, sm[w]);
-  return x;
+  float2 all = {0.0f, 0.0f};
+  for (int w = 0; w < THREADS / 32; ++w) {
+    all.x += sm[w].x;
+    all.y += sm[w].y;
+  }
+  return all;
 }
 
 __device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
@@ -502,85 +665,104 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
                         : static_cast<const float*>(a.teacher_logits)[i];
 }
 
-// One block per row. LOSS: statistics and losses from the logits; GRAD: the
-// gradient, from them or from the forward call's normalisers.
-template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
+// A row per block, or per cluster of a.split blocks (LOSS) or a.split
+// independent blocks (the gradient alone). LOSS: statistics and losses from the
+// logits; GRAD: the gradient, from them or from the forward call's normalisers.
+template <typename T, int THREADS, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
+__global__ void __launch_bounds__(THREADS, kResident / THREADS)
+    rows_kernel(const __grid_constant__ RowArgs a) {
   overlap_wait();
-  const int64_t r = blockIdx.x;
+  const int split = 1 << a.shift, rank = (int)(blockIdx.x & (unsigned)(split - 1));
+  const int64_t r = blockIdx.x >> a.shift;
   const int V = a.vocab, K = a.teacher_k, tid = threadIdx.x;
   const T* z = static_cast<const T*>(a.logits) + r * a.row_stride;
-  __shared__ float sm[kThreads / 32];
-  __shared__ Sums sm_sums[kThreads / 32];
+  const Part part = part_of(z, V, rank, a.shift);
+  // The first block of a row writes its statistics and losses.
+  const bool first = rank == 0, teacher = K > 0 && (GRAD || first);
+  // Whether this block needs the logit of a column: for the losses, or because
+  // it writes that column's gradient. (Another block's columns may have been
+  // overwritten in place when the gradient is computed alone.)
+  auto wanted = [&](int id) {
+    return id >= 0 && ((LOSS && first) || (id >= part.lo && id < part.hi));
+  };
+  __shared__ __align__(16) BlockSums sm_sums;
+  __shared__ __align__(16) Sums sm_part;
+  __shared__ float2 sm_add[THREADS / 32];
   __shared__ int32_t s_id[ZS_MAX_TEACHER + 1];
-  __shared__ float s_q[ZS_MAX_TEACHER], s_lnq[ZS_MAX_TEACHER], s_z[ZS_MAX_TEACHER + 1];
-  auto fmax_ = [](float x, float y) { return fmaxf(x, y); };
-  auto fadd_ = [](float x, float y) { return x + y; };
+  __shared__ float s_q[ZS_MAX_TEACHER], s_z[ZS_MAX_TEACHER + 1];
 
-  // The target (-1: none) and the teacher's record with its softmax q.
+  // The target (-1: none), and the teacher's record: ids, u = t / T in s_q, and
+  // the logits of those columns. Each thread keeps the entries that it wrote.
   int32_t target = -1;
   bool bad_target = false;
-  if (a.targets) {
-    const int64_t t = a.targets[r];
-    bad_target = t >= V;
-    if (bad_target && tid == 0) atomicOr(a.err, 1u);
-    target = t < 0 || bad_target ? -1 : (int32_t)t;
-  }
-  float Q = 0.0f;
-  if (K > 0) {
-    int32_t id = -1;
-    float u = -INFINITY;
-    if (tid < K) {
-      id = a.teacher_ids[r * K + tid];
-      if (id >= V) {
-        atomicOr(a.err, 1u);
-        id = -1;
+  float z_target = 0.0f, u_max = -INFINITY;
+  auto read_labels = [&]() {
+    if (teacher) {
+      for (int k = tid; k < K; k += THREADS) {
+        int32_t id = a.teacher_ids[r * K + k];
+        const float t = teacher_logit(a, r * K + k);
+        if (id >= V) {
+          if (first) atomicOr(a.err, 1u);
+          id = -1;
+        }
+        const float u = id >= 0 ? t * a.inv_t : -INFINITY;
+        s_id[k] = id;
+        s_q[k] = u;
+        s_z[k] = wanted(id) ? value_of(z[id]) : 0.0f;
+        u_max = fmaxf(u_max, u);
       }
-      if (id >= 0) u = teacher_logit(a, r * K + tid) * a.inv_t;
     }
-    float lnq;
-    if (a.teacher_lse) {
-      lnq = u - a.teacher_lse[r];
-    } else {
-      float m = block_reduce(u, sm, fmax_);
-      if (m == -INFINITY) m = 0.0f;
-      const float s = block_reduce(id >= 0 ? expf(u - m) : 0.0f, sm, fadd_);
-      lnq = u - m - logf(s);
+    if (a.targets) {
+      const int64_t t = a.targets[r];
+      bad_target = t >= V;
+      if (bad_target && first && tid == 0) atomicOr(a.err, 1u);
+      target = t < 0 || bad_target ? -1 : (int32_t)t;
     }
-    const float q = id >= 0 && u != -INFINITY ? expf(lnq) : 0.0f;
-    Q = block_reduce(q, sm, fadd_);
-    if (tid < K) {
-      s_id[tid] = id;
-      s_q[tid] = q;
-      s_lnq[tid] = lnq;
-      s_z[tid] = id >= 0 ? value_of(z[id]) : 0.0f;
+    z_target = wanted(target) ? value_of(z[target]) : 0.0f;
+    if (GRAD && tid == 0) {
+      s_id[K] = target;
+      s_z[K] = z_target;
     }
-  }
-  const float z_target = target >= 0 ? value_of(z[target]) : 0.0f;
-  if (GRAD && tid == 0) {
-    s_id[K] = target;
-    s_z[K] = z_target;
-  }
-  __syncthreads();
+  };
 
-  // Statistics.
-  float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f;
+  float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f, ln_s = 0.0f;
+  bool empty = false;
   if (LOSS) {
     extern __shared__ __align__(16) unsigned char dynamic[];
     TopShared* top = reinterpret_cast<TopShared*>(dynamic);
-    T* maxima = reinterpret_cast<T*>(top + 1);
+    T* maxima = nullptr;
+    if (TOP) {
+      const int capacity = min(kListed, V);
+      uint64_t* list = reinterpret_cast<uint64_t*>(top + 1);
+      maxima = reinterpret_cast<T*>(list + capacity);
+      if (tid == 0) {
+        top->capacity = capacity;
+        top->list = list;
+      }
+    }
     uint64_t best = 0;
-    const Sums t = row_sums<T, ENTROPY, OWN, TOP>(z, V, a.scale, a.slack, sm_sums, maxima, &best,
-                                                  a.err);
+    Sums t = part_sums<T, THREADS, ENTROPY, OWN, TOP>(z, part, a.scale, a.slack, &u_max, sm_sums,
+                                                      maxima, &best, a.err, read_labels);
+    // (block_sums waited for the table)
+    if (TOP) select_top<T, THREADS>(z, {part, maxima}, a.top_k, best, *top, a.err);
+    if (split > 1) {
+      if (tid == 0) sm_part = t;
+      cluster_arrive();
+      cluster_wait();
+      if (GRAD || first) t = cluster_sums(&sm_part, split, a.scale);
+      if (TOP && first) cluster_top<THREADS>(*top, a.top_k, split);
+      cluster_arrive();  // this block has read the others' shared memory
+    }
     const float m = t.m, U = t.u;
     M = m == -INFINITY ? 0.0f : m;  // a row masked throughout: every e is 2^-inf = 0
     S = t.s;
     S1 = OWN ? t.s1 : S;
-    const bool empty = m == -INFINITY && S == 0.0f;
-    const float ln_s = logf(S), ln_s1 = OWN ? logf(S1) : ln_s;
+    empty = m == -INFINITY && S == 0.0f;
+    ln_s = logf(S);
+    const float ln_s1 = OWN ? logf(S1) : ln_s;
     lse = empty ? -INFINITY : fmaf(M, a.inv_t, ln_s);
     lse1 = empty ? -INFINITY : M + ln_s1;
-    if (tid == 0) {
+    if (first && tid == 0) {
       if (a.lse) a.lse[r] = lse;
       if (a.hard_lse) a.hard_lse[r] = lse1;
       if (a.entropy) a.entropy[r] = empty ? 0.0f : ln_s - kLn2 * (U / S);
@@ -592,23 +774,42 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
                                         : (z_target - M) * t - (a.distill ? ln_s1 : ln_s);
       }
     }
-    if (a.loss) {
-      float l = 0.0f;
-      if (tid < K && !(s_q[tid] == 0.0f))
-        l = s_q[tid] * (s_lnq[tid] - (empty ? -INFINITY : (s_z[tid] - M) * a.inv_t - ln_s));
-      l = block_reduce(l, sm, fadd_);
-      if (tid == 0) a.loss[r] = l;
-    }
-    if (TOP) {
-      // block_sums waited for the table
-      select_top<T, kThreads>(z, {span_of(z, V), V, maxima}, a.top_k, best, *top, a.err);
-      for (int k = tid; k < a.top_k; k += kThreads) {
-        const int32_t id = (int32_t)~(uint32_t)top->best[k];
-        a.top_ids[r * a.top_k + k] = id;
+    if (TOP && first) {
+      for (int k = tid; k < a.top_k; k += THREADS) {
+        const uint64_t key = top->best[k];
+        a.top_ids[r * a.top_k + k] = (int32_t)~(uint32_t)key;
         a.top_logprobs[r * a.top_k + k] =
-            empty ? -INFINITY : (value_of(z[id]) - M) * a.inv_t - ln_s;
+            empty ? -INFINITY : (key_value<T>(key) - M) * a.inv_t - ln_s;
       }
     }
+  } else {
+    read_labels();
+    block_sums<THREADS>({0.0f, 0.0f, 0.0f, 0.0f}, 0.0f, &u_max, sm_sums);
+  }
+
+  // The teacher's q_k = x_k / X with x_k = exp(u_k - u_max), X their sum (or
+  // x_k = exp(u_k - teacher_lse), X = 1); Q = sum q. The loss in one more sum,
+  //   sum_k q_k (ln q_k - ln p_k) = (1/X) sum_k x_k (ln x_k - ln p_k) - Q ln X.
+  float Q = 0.0f, per_x = 1.0f;
+  if (teacher) {
+    const float u0 = a.teacher_lse ? a.teacher_lse[r] : u_max == -INFINITY ? 0.0f : u_max;
+    float x_sum = 0.0f, l_sum = 0.0f;
+    for (int k = tid; k < K; k += THREADS) {
+      const float ln_x = s_q[k] - u0, x = expf(ln_x);
+      s_q[k] = x;
+      x_sum += x;
+      if (LOSS && !(x == 0.0f))
+        l_sum += x * (ln_x - (empty ? -INFINITY : (s_z[k] - M) * a.inv_t - ln_s));
+    }
+    const float2 t = block_add<THREADS>(x_sum, l_sum, sm_add);
+    Q = t.x;
+    float loss = t.y;
+    if (!a.teacher_lse && !(Q == 0.0f)) {
+      per_x = 1.0f / Q;
+      loss = loss * per_x - logf(Q);
+      Q = Q * per_x;
+    }
+    if (LOSS && first && tid == 0 && a.loss) a.loss[r] = loss;
   }
 
   if (GRAD) {
@@ -651,21 +852,23 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     if (A == 0.0f && B == 0.0f) M = INFINITY;
     if (A1 == 0.0f) M1 = INFINITY;
     const GradRow row = {A, B, A1, M, M1, a.scale, zero};
-    write_row<T, ENTROPY, OWN>(z, g, V, row, a.err);
+    __syncthreads();  // the labels, before anything is overwritten in place
+    write_part<T, THREADS, ENTROPY, OWN>(z, g, part, row, a.err);
     __syncthreads();
     // The columns of the target and the teacher's ids, from the logits kept
     // above (z may be overwritten by now). Equal ids all store the same value.
-    for (int k = tid; k <= K; k += kThreads) {
+    for (int k = tid; k <= K; k += THREADS) {
       const int32_t id = s_id[k];
-      if (id < 0 || zero) continue;
+      if (id < part.lo || id >= part.hi || zero) continue;
       float q = 0.0f;
       for (int i = 0; i < K; ++i)
         if (s_id[i] == id) q += s_q[i];
-      float x = smooth<ENTROPY, OWN>(row, {s_z[k], 0.0f}).x - w * a.inv_t * q;
+      float x = smooth<ENTROPY, OWN>(row, {s_z[k], 0.0f}).x - w * a.inv_t * (q * per_x);
       if (id == target) x += at_target;
       store(g + id, x);
     }
   }
+  if (LOSS && split > 1) cluster_wait();  // the others have read this block's shared memory
 }
 
 RowArgs row_args(const VocabLaunch& in) {
@@ -703,15 +906,37 @@ RowArgs row_args(const VocabLaunch& in) {
   return a;
 }
 
-template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
-cudaError_t launch_rows(const VocabLaunch& in, cudaStream_t stream) {
-  const RowArgs a = row_args(in);
+// How many blocks share a row (1, 2, 4 or 8; a cluster when they must meet).
+//  - Few rows: until the blocks fill the GPU (the gradient alone: four times
+//    over), as long as every thread has a chunk.
+//  - Loss and gradient in one call: the rows in flight are read twice, so they
+//    are to stay in L2.
+//  - Top alternatives: the table of a block's part stays under a quarter of an
+//    SM's shared memory.
+template <typename T, bool LOSS, bool GRAD, bool TOP>
+int split_of(const VocabLaunch& in) {
+  const int64_t chunks = in.vocab / kPer<T>;
+  const int64_t blocks = kSMs * (kResident / kLong), fill = LOSS ? blocks : 4 * blocks;
+  int split = 1;
+  while (split < kMaxSplit && in.rows * split < fill && chunks >= 2 * split * kLong) split *= 2;
+  if (LOSS && GRAD)
+    while (split < kMaxSplit && blocks / split * in.vocab * (int64_t)sizeof(T) > kRowsInL2) split *= 2;
+  if (TOP)
+    while (split < kMaxSplit && chunks / split * (int64_t)sizeof(T) > kTableBytes) split *= 2;
+  return split;
+}
+
+template <typename T, int THREADS, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
+cudaError_t launch_rows(const VocabLaunch& in, int split, cudaStream_t stream) {
+  RowArgs a = row_args(in);
   if (!a.err) return cudaErrorInvalidSymbol;
-  const auto kernel = rows_kernel<T, LOSS, GRAD, ENTROPY, OWN, TOP>;
+  a.shift = split == 8 ? 3 : split / 2;
+  const auto kernel = rows_kernel<T, THREADS, LOSS, GRAD, ENTROPY, OWN, TOP>;
   size_t smem = 0;
   if (TOP) {
-    // A row's table has an entry for each 32 bytes of its logits and two ends.
-    smem = sizeof(TopShared) + (in.vocab / kPer<T> + 3) * sizeof(T);
+    // The table: an entry for each 32 bytes of the part, and two ends.
+    smem = sizeof(TopShared) + (in.vocab < kListed ? in.vocab : kListed) * 8 +
+           (in.vocab / kPer<T> / split + 4) * sizeof(T);
     static std::atomic<bool> allowed[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -722,14 +947,23 @@ cudaError_t launch_rows(const VocabLaunch& in, cudaStream_t stream) {
       allowed[dev & 63].store(true, std::memory_order_release);
     }
   }
-  return launch_kernel(kernel, dim3((unsigned)in.rows), dim3(kThreads), smem, stream, a);
+  return launch_clusters(LOSS ? split : 1, kernel, dim3((unsigned)(in.rows * split)),
+                         dim3(THREADS), smem, stream, a);
+}
+
+template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
+cudaError_t launch_typed(const VocabLaunch& in, cudaStream_t stream) {
+  if (in.vocab / kPer<T> <= kShortChunks)
+    return launch_rows<T, kShort, LOSS, GRAD, ENTROPY, OWN, TOP>(in, 1, stream);
+  return launch_rows<T, kLong, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split_of<T, LOSS, GRAD, TOP>(in),
+                                                              stream);
 }
 
 template <bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
 cudaError_t launch(const VocabLaunch& in, cudaStream_t stream) {
   return in.dtype == ZS_BF16
-             ? launch_rows<__nv_bfloat16, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream)
-             : launch_rows<float, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream);
+             ? launch_typed<__nv_bfloat16, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream)
+             : launch_typed<float, LOSS, GRAD, ENTROPY, OWN, TOP>(in, stream);
 }
 
 // The hard labels need a softmax of their own: T is not 1, and one of their

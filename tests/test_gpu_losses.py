@@ -90,7 +90,7 @@ def _check_logprobs(R, V, dtype, T=1.0, stride=None, lead=0, k=0, mask=None, z=N
 
 
 VOCABS = [1, 2, 3, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 65, 127, 129, 255, 257, 511, 1000, 1023,
-          2049, 4095, 4099, 8191, 8209, 16385, 32000, 50257, 65537, 151936, 262147]
+          2049, 4095, 4099, 8191, 8209, 16385, 32000, 50257, 65537, 151936, 262147, 1048576]
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
