@@ -337,6 +337,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
   // then one thread reads each of them again, so that all their loads are in
   // flight together. More than fit are counted, not listed.
   auto list_from = [&](uint64_t bound, bool look) {
+    __syncthreads();  // total_of's last answer has been read
     if (tid == 0) sh.count = sh.total = 0;
     __syncthreads();
     const float at_least = key_value<T>(bound);
@@ -383,7 +384,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     return sh.count;
   };
   uint64_t bound =
-      bound_of<T>(k, 2 * k, [&](uint64_t b) { return __syncthreads_count(mine >= b); });
+      bound_of<T>(k, k + k / 4 + 2, [&](uint64_t b) { return __syncthreads_count(mine >= b); });
   int n = list_from(bound, mine >= bound);
   if (n > sh.capacity) {
     // Very many in a few threads' chunks: the exact k-th best chunk leaves the
@@ -525,12 +526,11 @@ __device__ __forceinline__ Sums cluster_sums(const Sums* mine, int split, float 
 template <int THREADS>
 __device__ __forceinline__ void cluster_top(TopShared& sh, int k, int split) {
   const int tid = threadIdx.x;
-  static_assert(kMaxSplit * 32 <= kLong, "a warp for each block's list");
-  const int own = tid >> 5, lane = tid & 31;
-  if (own < split)
+  const int lane = tid & 31;
+  for (int own = tid >> 5; own < split; own += THREADS / 32)  // a warp for each block's list
     for (int i = lane; i < k; i += 32) sh.list[own * k + i] = remote_key(sh.best + i, own);
   __syncthreads();
-  if (own < split) {
+  for (int own = tid >> 5; own < split; own += THREADS / 32) {
     for (int i = lane; i < k; i += 32) {
       const uint64_t key = sh.list[own * k + i];
       int above[kMaxSplit] = {};

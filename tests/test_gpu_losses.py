@@ -189,6 +189,18 @@ def test_top_alternatives(k, dtype):
     _check_logprobs(2, 151936, dtype, k=k, z=z)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_top_alternatives_of_many_rows(dtype):
+    """Thousands of rows whose largest values gather in few threads' chunks, so
+    that the exact search over the whole table runs in every block."""
+    R, V = 2500, 20011
+    z = torch.randn(R, V, generator=torch.Generator().manual_seed(2))
+    for i in range(16):
+        z[:, i::4096] += 8.0
+    _check_logprobs(R, V, dtype, k=128, z=z)
+    _check_logprobs(R, V, dtype, k=40, z=z)
+
+
 def test_logprobs_each_output_alone_and_other_streams():
     R, V = 37, 5003
     _, view, z64, g = _rows(R, V, V, BF16)
