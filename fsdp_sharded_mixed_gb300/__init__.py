@@ -285,10 +285,20 @@ def _step_sizes(fn, plan, lo, hi, grad_slices, grad_dtype, states, out, param_dt
         _need(accum, S * 4, fn, "accum")
 
 
+_raw_stream = None  # (device -> its current stream's handle, current device) of torch
+
+
 def _stream(stream):
+    """A stream argument's handle; None = the current stream of the current
+    device, asked of torch without making a Stream object (3 us a call)."""
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()  # initialises, or raises without a device
+            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        current, device = _raw_stream
+        return current(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -550,12 +560,13 @@ def _rows_ptr(x, rows, vocab, stride, dtype, fn, name):
     return _ptr(x)
 
 
-def _rows_sizes(fn, rows, *named):
-    """(name, buffer, bytes per row) of the per-row buffers of a loss call."""
-    for name, x, nbytes in named:
-        if x is not None and not isinstance(x, int) and x.nbytes < rows * nbytes:
-            raise ValueError(f"{fn}: {name} holds {x.nbytes} bytes, the call needs "
-                             f"{rows * nbytes}")
+def _row_ptr(x, nbytes, fn, name):
+    """Address of a per-row buffer that must hold ``nbytes`` (None = not given)."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.nbytes < nbytes:
+        raise ValueError(f"{fn}: {name} holds {x.nbytes} bytes, the call needs {nbytes}")
+    return _ptr(x)
 
 
 def zs_token_logprobs(logits, dtype, rows, vocab, row_stride, targets, temperature=1.0,
@@ -565,34 +576,34 @@ def zs_token_logprobs(logits, dtype, rows, vocab, row_stride, targets, temperatu
     ``row_stride`` elements apart), the log probability of ``targets[r]`` (int64;
     negative = none), the entropy, the log-sum-exp and the ``top_k`` most likely
     ids (int32) with their log probabilities; fp32 outputs, None = not wanted."""
-    fn = "zs_token_logprobs"
-    _rows_sizes(fn, rows, ("targets", targets, 8), ("logprob", logprob, 4),
-                ("entropy", entropy, 4), ("lse", lse, 4), ("top_ids", top_ids, 4 * top_k),
-                ("top_logprobs", top_logprobs, 4 * top_k))
+    fn, n = "zs_token_logprobs", 4 * rows
     _check(lib().zs_token_logprobs(
         _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
-        row_stride, _ptr(targets), temperature, _ptr(logprob), _ptr(entropy), _ptr(lse), top_k,
-        _ptr(top_ids), _ptr(top_logprobs), _stream(stream)))
+        row_stride, _row_ptr(targets, 2 * n, fn, "targets"), temperature,
+        _row_ptr(logprob, n, fn, "logprob"), _row_ptr(entropy, n, fn, "entropy"),
+        _row_ptr(lse, n, fn, "lse"), top_k, _row_ptr(top_ids, n * top_k, fn, "top_ids"),
+        _row_ptr(top_logprobs, n * top_k, fn, "top_logprobs"), _stream(stream)))
 
 
 def zs_token_logprobs_grad(logits, dtype, rows, vocab, row_stride, targets, temperature, lse,
                            entropy, d_logprob, d_entropy, d_logits, grad_stride, stream=None):
     """Enqueue the gradient of ``zs_token_logprobs``' logprob and entropy into
     ``d_logits`` (the logits' dtype; may be the logits themselves)."""
-    fn = "zs_token_logprobs_grad"
-    _rows_sizes(fn, rows, ("targets", targets, 8), ("lse", lse, 4), ("entropy", entropy, 4),
-                ("d_logprob", d_logprob, 4), ("d_entropy", d_entropy, 4))
+    fn, n = "zs_token_logprobs_grad", 4 * rows
     _check(lib().zs_token_logprobs_grad(
         _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
-        row_stride, _ptr(targets), temperature, _ptr(lse), _ptr(entropy), _ptr(d_logprob),
-        _ptr(d_entropy), _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"),
-        grad_stride, _stream(stream)))
+        row_stride, _row_ptr(targets, 2 * n, fn, "targets"), temperature,
+        _row_ptr(lse, n, fn, "lse"), _row_ptr(entropy, n, fn, "entropy"),
+        _row_ptr(d_logprob, n, fn, "d_logprob"), _row_ptr(d_entropy, n, fn, "d_entropy"),
+        _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"), grad_stride,
+        _stream(stream)))
 
 
-def _teacher_sizes(fn, rows, ids, logits, dtype, k, lse):
-    _rows_sizes(fn, rows, ("teacher_ids", ids, 4 * k),
-                ("teacher_logits", logits, ELEM_BYTES.get(dtype, 0) * k),
-                ("teacher_lse", lse, 4))
+def _record(fn, rows, ids, logits, dtype, k, lse):
+    """A teacher's record as the C calls take it."""
+    return (_row_ptr(ids, 4 * rows * k, fn, "teacher_ids"),
+            _row_ptr(logits, ELEM_BYTES.get(dtype, 0) * rows * k, fn, "teacher_logits"), dtype, k,
+            _row_ptr(lse, 4 * rows, fn, "teacher_lse"))
 
 
 def zs_distill_loss(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
@@ -601,15 +612,14 @@ def zs_distill_loss(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher
     """Enqueue the distillation loss of each row against the teacher's
     ``teacher_k`` recorded entries (int32 ids, negative = unused; logits of
     ``teacher_dtype``), and with ``targets`` the hard labels' log probability."""
-    fn = "zs_distill_loss"
-    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
-    _rows_sizes(fn, rows, ("targets", targets, 8), ("loss", loss, 4), ("lse", lse, 4),
-                ("logprob", logprob, 4), ("hard_lse", hard_lse, 4))
+    fn, n = "zs_distill_loss", 4 * rows
     _check(lib().zs_distill_loss(
         _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
-        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
-        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(loss), _ptr(lse), _ptr(logprob),
-        _ptr(hard_lse), _stream(stream)))
+        row_stride, *_record(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k,
+                             teacher_lse), temperature, _row_ptr(targets, 2 * n, fn, "targets"),
+        _row_ptr(loss, n, fn, "loss"), _row_ptr(lse, n, fn, "lse"),
+        _row_ptr(logprob, n, fn, "logprob"), _row_ptr(hard_lse, n, fn, "hard_lse"),
+        _stream(stream)))
 
 
 def zs_distill_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
@@ -617,16 +627,15 @@ def zs_distill_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher
                     d_loss, d_logprob, d_logits, grad_stride, stream=None):
     """Enqueue the gradient of ``zs_distill_loss``' loss and logprob into
     ``d_logits`` (the logits' dtype; may be the logits themselves)."""
-    fn = "zs_distill_grad"
-    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
-    _rows_sizes(fn, rows, ("targets", targets, 8), ("lse", lse, 4), ("hard_lse", hard_lse, 4),
-                ("d_loss", d_loss, 4), ("d_logprob", d_logprob, 4))
+    fn, n = "zs_distill_grad", 4 * rows
     _check(lib().zs_distill_grad(
         _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
-        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
-        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(lse), _ptr(hard_lse), _ptr(d_loss),
-        _ptr(d_logprob), _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"),
-        grad_stride, _stream(stream)))
+        row_stride, *_record(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k,
+                             teacher_lse), temperature, _row_ptr(targets, 2 * n, fn, "targets"),
+        _row_ptr(lse, n, fn, "lse"), _row_ptr(hard_lse, n, fn, "hard_lse"),
+        _row_ptr(d_loss, n, fn, "d_loss"), _row_ptr(d_logprob, n, fn, "d_logprob"),
+        _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"), grad_stride,
+        _stream(stream)))
 
 
 def zs_distill_loss_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, teacher_logits,
@@ -635,16 +644,14 @@ def zs_distill_loss_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, te
                          stream=None):
     """``zs_distill_loss`` and its gradient in one call, the logits read from
     HBM once; ``teacher_k`` = 0: cross entropy of the targets alone."""
-    fn = "zs_distill_loss_grad"
-    _teacher_sizes(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k, teacher_lse)
-    _rows_sizes(fn, rows, ("targets", targets, 8), ("loss", loss, 4), ("lse", lse, 4),
-                ("logprob", logprob, 4), ("hard_lse", hard_lse, 4), ("d_loss", d_loss, 4),
-                ("d_logprob", d_logprob, 4))
+    fn, n = "zs_distill_loss_grad", 4 * rows
     _check(lib().zs_distill_loss_grad(
         _rows_ptr(logits, rows, vocab, row_stride, dtype, fn, "logits"), dtype, rows, vocab,
-        row_stride, _ptr(teacher_ids), _ptr(teacher_logits), teacher_dtype, teacher_k,
-        _ptr(teacher_lse), temperature, _ptr(targets), _ptr(d_loss), _ptr(d_logprob),
-        _ptr(loss), _ptr(lse), _ptr(logprob), _ptr(hard_lse),
+        row_stride, *_record(fn, rows, teacher_ids, teacher_logits, teacher_dtype, teacher_k,
+                             teacher_lse), temperature, _row_ptr(targets, 2 * n, fn, "targets"),
+        _row_ptr(d_loss, n, fn, "d_loss"), _row_ptr(d_logprob, n, fn, "d_logprob"),
+        _row_ptr(loss, n, fn, "loss"), _row_ptr(lse, n, fn, "lse"),
+        _row_ptr(logprob, n, fn, "logprob"), _row_ptr(hard_lse, n, fn, "hard_lse"),
         _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"), grad_stride,
         _stream(stream)))
 
