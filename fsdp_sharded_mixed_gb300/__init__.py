@@ -555,17 +555,20 @@ def _rows_ptr(x, rows, vocab, stride, dtype, fn, name):
         if x.shape[0] < rows or x.shape[1] < vocab:
             raise ValueError(f"{fn}: {name} is {tuple(x.shape)}, the call needs {(rows, vocab)}")
         return x.data_ptr()
-    if rows > 0:
-        _need(x, ((rows - 1) * stride + vocab) * size, fn, name)
-    return _ptr(x)
+    return _row_ptr(x, ((rows - 1) * stride + vocab) * size if rows > 0 else 0, fn, name)
 
 
 def _row_ptr(x, nbytes, fn, name):
-    """Address of a per-row buffer that must hold ``nbytes`` (None = not given)."""
-    if x is None or isinstance(x, int):
-        return x
-    if x.nbytes < nbytes:
-        raise ValueError(f"{fn}: {name} holds {x.nbytes} bytes, the call needs {nbytes}")
+    """Address of a buffer that must hold ``nbytes`` (None = not given). These
+    calls take a dozen; a dense tensor that is long enough takes one test."""
+    if x is None:
+        return None
+    try:
+        if x.nbytes >= nbytes and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:  # an address, or a numpy array
+        pass
+    _need(x, nbytes, fn, name)
     return _ptr(x)
 
 

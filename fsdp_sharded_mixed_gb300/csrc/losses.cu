@@ -29,12 +29,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kLong = 256, kShort = 32;  // threads of a row's block
+constexpr int kMaxThreads = 256;         // of a row's block (32, 64, 128 or 256)
 constexpr int kResident = 1024;          // threads of an SM: 64 registers each
 constexpr int kSMs = 152;
 constexpr int kMaxSplit = 8;               // blocks of a row: the portable cluster size
-constexpr int kShortChunks = 256;         // rows up to this many go to one warp each
-constexpr int64_t kRowsInL2 = 64 << 20;   // bytes of rows in flight that L2 (129 MB) keeps
+constexpr int64_t kRowsInL2 = 96 << 20;   // bytes of rows in flight that L2 (129 MB) keeps
 constexpr int64_t kTableBytes = 40 << 10;
 constexpr int kMaxSmem = 200 * 1024;      // dynamic shared memory of a block
 
@@ -92,12 +91,25 @@ __device__ __forceinline__ Part part_of(const T* z, int V, int rank, int shift) 
   return p;
 }
 
+// How long L2 should hold what a load brings: as ever; until it is read again
+// (a row whose gradient follows its sums); no longer.
+enum Hold { kUsual, kUntilRead, kOnce };
+template <Hold HOLD>
 __device__ __forceinline__ void load_chunk(uint32_t* w, const void* p) {
-  asm volatile("ld.global.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                 "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
+#define ZS_LOAD_CHUNK(hold)                                                                    \
+  asm volatile("ld.global.L1::no_allocate" hold                                                \
+               ".v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"                               \
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),       \
+                 "=r"(w[6]), "=r"(w[7])                                                        \
+               : "l"(p)                                                                        \
+               : "memory")
+  if (HOLD == kUsual)
+    ZS_LOAD_CHUNK("");
+  else if (HOLD == kUntilRead)
+    ZS_LOAD_CHUNK(".L2::evict_last");
+  else
+    ZS_LOAD_CHUNK(".L2::evict_first");
+#undef ZS_LOAD_CHUNK
 }
 // Elements 2i and 2i+1 of a chunk.
 __device__ __forceinline__ float2 pair_of(const uint32_t* w, int i, __nv_bfloat16) {
@@ -196,50 +208,49 @@ struct Sums {
 __device__ __forceinline__ float toward(float m, float M, float scale) {
   return M == -INFINITY ? 0.0f : clamped((m - M) * scale);
 }
+template <bool OWN>
 __device__ __forceinline__ Sums moved(const Sums& a, float M, float scale) {
   const float delta = toward(a.m, M, scale), f = exp2_fast(delta);
-  const float f1 = exp2_fast(toward(a.m, M, kLog2e));
+  const float f1 = OWN ? exp2_fast(toward(a.m, M, kLog2e)) : 0.0f;
   return {M, f * a.s, f * fmaf(a.s, delta, a.u), f1 * a.s1};
 }
 
 // The block's sums, in a fixed order, and the largest of its u; every thread
 // gets them.
 struct BlockSums {
-  Sums sums[kLong / 32];
-  float u[kLong / 32];
+  Sums sums[kMaxThreads / 32];
+  float u[kMaxThreads / 32];
 };
-template <int THREADS>
-__device__ __forceinline__ Sums block_sums(Sums t, float scale, float* u, BlockSums& sm) {
+// The sums of groups of n lanes (a power of two), in a fixed order.
+template <bool ENTROPY, bool OWN>
+__device__ __forceinline__ Sums lane_sums(Sums t, int n, float scale) {
   float M = t.m;
-  for (int off = 16; off > 0; off >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-    *u = fmaxf(*u, __shfl_xor_sync(0xFFFFFFFFu, *u, off));
-  }
-  t = moved(t, M, scale);
-  for (int off = 16; off > 0; off >>= 1) {
+  for (int off = n / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+  t = moved<OWN>(t, M, scale);
+  for (int off = n / 2; off > 0; off >>= 1) {
     t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, off);
-    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
-    t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
+    if (ENTROPY) t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
+    if (OWN) t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
   }
+  return t;
+}
+__device__ __forceinline__ float lane_max(float x, int n) {
+  for (int off = n / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+  return x;
+}
+template <int THREADS, bool ENTROPY, bool OWN>
+__device__ __forceinline__ Sums block_sums(Sums t, float scale, float* u, BlockSums& sm) {
+  constexpr int kWarps = THREADS / 32;
+  t = lane_sums<ENTROPY, OWN>(t, 32, scale);
+  *u = lane_max(*u, 32);
   if ((threadIdx.x & 31) == 0) {
     sm.sums[threadIdx.x >> 5] = t;
     sm.u[threadIdx.x >> 5] = *u;
   }
   __syncthreads();
   if (THREADS == 32) return t;
-  M = sm.sums[0].m;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    M = fmaxf(M, sm.sums[w].m);
-    *u = fmaxf(*u, sm.u[w]);
-  }
-  Sums all = {M, 0.0f, 0.0f, 0.0f};
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const Sums x = moved(sm.sums[w], M, scale);
-    all.s += x.s;
-    all.u += x.u;
-    all.s1 += x.s1;
-  }
-  return all;
+  *u = lane_max(sm.u[threadIdx.x % kWarps], kWarps);
+  return lane_sums<ENTROPY, OWN>(sm.sums[threadIdx.x % kWarps], kWarps, scale);
 }
 
 // ---- the top alternatives -------------------------------------------------------
@@ -271,13 +282,15 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 // Table entry p: body chunk p; then the tail and the head (whose position comes
 // first). An end without elements has key 0. Entry p belongs to thread p modulo
 // the block.
-constexpr int kListed = 2048;  // elements that are ranked; 16 * ZS_MAX_TOP at least
+// Elements that may be ranked: those of k chunks at least, and enough for the
+// sorted lists of a row's blocks.
+__host__ __device__ __forceinline__ int list_capacity(int k) { return 16 * (k < 16 ? 16 : k); }
 constexpr int kFound = 512;    // chunks that are read again; ZS_MAX_TOP at least
 struct TopShared {
   uint64_t best[ZS_MAX_TOP];
   int found[kFound];
   int count, total;
-  int capacity;    // of the list: kListed, or the whole of a shorter row
+  int capacity;    // of the list
   uint64_t* list;  // after this, then the table
 };
 // A bound that at least k of the keys reach, and at most `most` where unique
@@ -358,7 +371,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
       float x[kPer<T>];
       if (p < ch.sp.body) {
         uint32_t w[kWords];
-        load_chunk(w, z + lo);
+        load_chunk<kUsual>(w, z + lo);
 #pragma unroll
         for (int i = 0; i < kPer<T> / 2; ++i) {
           x[2 * i] = pair_of(w, i, T()).x;
@@ -397,7 +410,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     n = list_from(bound, true);
   }
   bound = 0;
-  if (n > kListed / 4)  // ranking is quadratic: first the exact k-th best
+  if (n > 512)  // ranking is quadratic: first the exact k-th best
     bound = bound_of<T>(k, k, [&](uint64_t b) {
       int reach = 0;
       for (int i = tid; i < n; i += THREADS) reach += sh.list[i] >= b;
@@ -418,11 +431,13 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
 // flight ahead of those that it works on. TOP: the table, and the thread's best
 // chunk.
 constexpr int kFlight = 2;
-// between(): run while the first chunks are on their way; gives u.
-template <typename T, int THREADS, bool ENTROPY, bool OWN, bool TOP, typename F>
+// labels: its read() asks for a row's labels once the first chunks are on their
+// way, gather() for the logits that they name after the first of them were used,
+// finish() puts all in place and gives the thread's u.
+template <typename T, int THREADS, bool ENTROPY, bool OWN, bool TOP, Hold HOLD, typename L>
 __device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scale, float slack,
-                                          float* u, BlockSums& sm, T* maxima, uint64_t* best,
-                                          unsigned int* err, F between) {
+                                          BlockSums& sm, T* maxima, uint64_t* best, float* u,
+                                          unsigned int* err, L& labels) {
   const int tid = threadIdx.x;
   const T* body = z + sp.lo + sp.head;
   Stats<ENTROPY, OWN> st;
@@ -434,11 +449,11 @@ __device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scal
       const int64_t at = (int64_t)q * kPer<T>;
       if (q < sp.body && within(sp.lo + sp.head + at, sp.lo + sp.head + at + kPer<T>, sp.lo,
                                 sp.hi, err))
-        load_chunk(w[f], body + at);
+        load_chunk<HOLD>(w[f], body + at);
     }
   };
   load(now, 0);
-  between();
+  labels.read();
   if (tid < sp.head) st.add_one(value_of(z[tid]), scale, slack);
   if (tid < sp.tail) st.add_one(value_of(z[sp.hi - sp.tail + tid]), scale, slack);
   if (TOP && tid < 32) {
@@ -465,12 +480,15 @@ __device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scal
           *best = max(*best, rank_key<T>(cm, sp.chunk0 + p + 1));
         }
       }
+    if (q0 == 0) labels.gather();
 #pragma unroll
     for (int f = 0; f < kFlight; ++f)
 #pragma unroll
       for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
   }
-  return block_sums<THREADS>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
+  if (sp.body == 0) labels.gather();
+  *u = labels.finish();
+  return block_sums<THREADS, ENTROPY, OWN>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
                              u, sm);
 }
 
@@ -504,20 +522,10 @@ __device__ __forceinline__ uint64_t remote_key(const uint64_t* p, int rank) {
   return x;
 }
 
-// The row's sums from its blocks': lane i of every warp reads block i's, and
-// each warp adds them in the same order.
+// The row's sums from its blocks': lane i of every warp reads block i's.
+template <bool ENTROPY, bool OWN>
 __device__ __forceinline__ Sums cluster_sums(const Sums* mine, int split, float scale) {
-  const int lane = threadIdx.x & 31;
-  Sums t = remote_sums(mine, lane & (split - 1));
-  float M = t.m;
-  for (int off = 1; off < split; off *= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-  t = moved(t, M, scale);
-  for (int off = 1; off < split; off *= 2) {
-    t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, off);
-    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, off);
-    t.s1 += __shfl_xor_sync(0xFFFFFFFFu, t.s1, off);
-  }
-  return t;
+  return lane_sums<ENTROPY, OWN>(remote_sums(mine, threadIdx.x & (split - 1)), split, scale);
 }
 
 // The row's top k from its blocks' sorted lists, into sh.best of this block: a
@@ -578,8 +586,9 @@ __device__ __forceinline__ void put_pair(uint32_t* w, int i, float2 g, float) {
   w[2 * i] = __float_as_uint(g.x);
   w[2 * i + 1] = __float_as_uint(g.y);
 }
+// (a gradient is not read again soon)
 __device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+  asm volatile("st.global.L2::evict_first.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
@@ -620,7 +629,7 @@ __device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, con
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       const int q = q0 + f * THREADS + tid;
-      if (in_row(q)) load_chunk(w[f], zb + (int64_t)q * kPer<T>);
+      if (in_row(q)) load_chunk<kOnce>(w[f], zb + (int64_t)q * kPer<T>);
     }
   };
   load(now, 0);
@@ -660,10 +669,88 @@ __device__ __forceinline__ float2 block_add(float x, float y, float2* sm) {
   return all;
 }
 
-__device__ __forceinline__ float teacher_logit(const RowArgs& a, int64_t i) {
-  return a.teacher_bf16 ? value_of(static_cast<const __nv_bfloat16*>(a.teacher_logits)[i])
-                        : static_cast<const float*>(a.teacher_logits)[i];
+// A teacher's logit as it is stored, and its value.
+__device__ __forceinline__ uint32_t teacher_bits(const RowArgs& a, int64_t i) {
+  return a.teacher_bf16 ? static_cast<const uint16_t*>(a.teacher_logits)[i]
+                        : static_cast<const uint32_t*>(a.teacher_logits)[i];
 }
+__device__ __forceinline__ float teacher_logit(const RowArgs& a, uint32_t bits) {
+  return __uint_as_float(a.teacher_bf16 ? bits << 16 : bits);
+}
+
+// A row's labels: the target (-1: none), and the teacher's record with the
+// logits of its columns. The loads of thread k's entry are issued, and waited
+// for, in three steps between which the block does other work; a record longer
+// than the block is read in the last one.
+struct LabelsShared {
+  int32_t id[ZS_MAX_TEACHER + 4];  // the teacher's ids and the target, then -1 up to a multiple of 4
+  float q[ZS_MAX_TEACHER];         // u = t / T (-inf: unused), then x_k = exp(u - u_max)
+  float z[ZS_MAX_TEACHER + 1];
+};
+template <typename T, int THREADS, bool LOSS, bool GRAD>
+struct Labels {
+  const RowArgs& a;
+  const T* z;
+  const int64_t r;
+  const Part& part;
+  const bool first, teacher;
+  LabelsShared& sh;
+  int32_t my_id = -1, target = -1;
+  int64_t raw_target = -1;
+  uint32_t my_t = 0;
+  float my_z = 0.0f, z_target = 0.0f;
+  bool bad_target = false;
+
+  // Whether this block needs the logit of a column: for the losses, or because
+  // it writes that column's gradient. (Another block's columns may have been
+  // overwritten in place when the gradient is computed alone.)
+  __device__ __forceinline__ bool wanted(int32_t id) const {
+    return id >= 0 && ((LOSS && first) || (id >= part.lo && id < part.hi));
+  }
+  __device__ __forceinline__ int32_t checked(int32_t id) const {
+    if (id < a.vocab) return id;
+    if (first) atomicOr(a.err, 1u);
+    return -1;
+  }
+  __device__ __forceinline__ void put(int k, int32_t id, uint32_t t, float zk, float* u) {
+    sh.id[k] = id;
+    sh.q[k] = id >= 0 ? teacher_logit(a, t) * a.inv_t : -INFINITY;
+    sh.z[k] = zk;
+    *u = fmaxf(*u, sh.q[k]);
+  }
+  __device__ __forceinline__ void read() {
+    const int k = threadIdx.x;
+    if (teacher && k < a.teacher_k) {
+      my_id = a.teacher_ids[r * a.teacher_k + k];
+      my_t = teacher_bits(a, r * a.teacher_k + k);
+    }
+    if (a.targets) raw_target = a.targets[r];
+  }
+  __device__ __forceinline__ void gather() {
+    my_id = checked(my_id);
+    if (wanted(my_id)) my_z = value_of(z[my_id]);
+    bad_target = raw_target >= a.vocab;
+    if (bad_target && first && threadIdx.x == 0) atomicOr(a.err, 1u);
+    if (raw_target >= 0 && !bad_target) target = (int32_t)raw_target;
+    if (wanted(target)) z_target = value_of(z[target]);
+  }
+  __device__ __forceinline__ float finish() {
+    const int K = a.teacher_k, tid = threadIdx.x;
+    float u = -INFINITY;
+    if (teacher) {
+      if (tid < K) put(tid, my_id, my_t, my_z, &u);
+      for (int k = tid + THREADS; k < K; k += THREADS) {
+        const int32_t id = checked(a.teacher_ids[r * K + k]);
+        put(k, id, teacher_bits(a, r * K + k), wanted(id) ? value_of(z[id]) : 0.0f, &u);
+      }
+    }
+    if (GRAD && tid < 4) {
+      sh.id[K + tid] = tid == 0 ? target : -1;
+      if (tid == 0) sh.z[K] = z_target;
+    }
+    return u;
+  }
+};
 
 // A row per block, or per cluster of a.split blocks (LOSS) or a.split
 // independent blocks (the gradient alone). LOSS: statistics and losses from the
@@ -679,51 +766,12 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
   const Part part = part_of(z, V, rank, a.shift);
   // The first block of a row writes its statistics and losses.
   const bool first = rank == 0, teacher = K > 0 && (GRAD || first);
-  // Whether this block needs the logit of a column: for the losses, or because
-  // it writes that column's gradient. (Another block's columns may have been
-  // overwritten in place when the gradient is computed alone.)
-  auto wanted = [&](int id) {
-    return id >= 0 && ((LOSS && first) || (id >= part.lo && id < part.hi));
-  };
   __shared__ __align__(16) BlockSums sm_sums;
   __shared__ __align__(16) Sums sm_part;
   __shared__ float2 sm_add[THREADS / 32];
-  __shared__ int32_t s_id[ZS_MAX_TEACHER + 1];
-  __shared__ float s_q[ZS_MAX_TEACHER], s_z[ZS_MAX_TEACHER + 1];
-
-  // The target (-1: none), and the teacher's record: ids, u = t / T in s_q, and
-  // the logits of those columns. Each thread keeps the entries that it wrote.
-  int32_t target = -1;
-  bool bad_target = false;
-  float z_target = 0.0f, u_max = -INFINITY;
-  auto read_labels = [&]() {
-    if (teacher) {
-      for (int k = tid; k < K; k += THREADS) {
-        int32_t id = a.teacher_ids[r * K + k];
-        const float t = teacher_logit(a, r * K + k);
-        if (id >= V) {
-          if (first) atomicOr(a.err, 1u);
-          id = -1;
-        }
-        const float u = id >= 0 ? t * a.inv_t : -INFINITY;
-        s_id[k] = id;
-        s_q[k] = u;
-        s_z[k] = wanted(id) ? value_of(z[id]) : 0.0f;
-        u_max = fmaxf(u_max, u);
-      }
-    }
-    if (a.targets) {
-      const int64_t t = a.targets[r];
-      bad_target = t >= V;
-      if (bad_target && first && tid == 0) atomicOr(a.err, 1u);
-      target = t < 0 || bad_target ? -1 : (int32_t)t;
-    }
-    z_target = wanted(target) ? value_of(z[target]) : 0.0f;
-    if (GRAD && tid == 0) {
-      s_id[K] = target;
-      s_z[K] = z_target;
-    }
-  };
+  __shared__ __align__(16) LabelsShared sl;
+  Labels<T, THREADS, LOSS, GRAD> labels = {a, z, r, part, first, teacher, sl};
+  float u_max = -INFINITY;
 
   float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f, ln_s = 0.0f;
   bool empty = false;
@@ -732,7 +780,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     TopShared* top = reinterpret_cast<TopShared*>(dynamic);
     T* maxima = nullptr;
     if (TOP) {
-      const int capacity = min(kListed, V);
+      const int capacity = list_capacity(a.top_k);
       uint64_t* list = reinterpret_cast<uint64_t*>(top + 1);
       maxima = reinterpret_cast<T*>(list + capacity);
       if (tid == 0) {
@@ -741,15 +789,15 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
       }
     }
     uint64_t best = 0;
-    Sums t = part_sums<T, THREADS, ENTROPY, OWN, TOP>(z, part, a.scale, a.slack, &u_max, sm_sums,
-                                                      maxima, &best, a.err, read_labels);
+    Sums t = part_sums<T, THREADS, ENTROPY, OWN, TOP, GRAD ? kUntilRead : kUsual>(
+        z, part, a.scale, a.slack, sm_sums, maxima, &best, &u_max, a.err, labels);
     // (block_sums waited for the table)
     if (TOP) select_top<T, THREADS>(z, {part, maxima}, a.top_k, best, *top, a.err);
     if (split > 1) {
       if (tid == 0) sm_part = t;
       cluster_arrive();
       cluster_wait();
-      if (GRAD || first) t = cluster_sums(&sm_part, split, a.scale);
+      if (GRAD || first) t = cluster_sums<ENTROPY, OWN>(&sm_part, split, a.scale);
       if (TOP && first) cluster_top<THREADS>(*top, a.top_k, split);
       cluster_arrive();  // this block has read the others' shared memory
     }
@@ -768,10 +816,10 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
       if (a.entropy) a.entropy[r] = empty ? 0.0f : ln_s - kLn2 * (U / S);
       if (a.logprob) {
         const float t = a.distill ? 1.0f : a.inv_t;
-        a.logprob[r] = bad_target       ? NAN
-                       : target < 0     ? 0.0f
-                       : empty          ? -INFINITY
-                                        : (z_target - M) * t - (a.distill ? ln_s1 : ln_s);
+        a.logprob[r] = labels.bad_target   ? NAN
+                       : labels.target < 0 ? 0.0f
+                       : empty             ? -INFINITY
+                                           : (labels.z_target - M) * t - (a.distill ? ln_s1 : ln_s);
       }
     }
     if (TOP && first) {
@@ -783,8 +831,10 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
       }
     }
   } else {
-    read_labels();
-    block_sums<THREADS>({0.0f, 0.0f, 0.0f, 0.0f}, 0.0f, &u_max, sm_sums);
+    labels.read();
+    labels.gather();
+    u_max = labels.finish();
+    block_sums<THREADS, false, false>({0.0f, 0.0f, 0.0f, 0.0f}, 0.0f, &u_max, sm_sums);
   }
 
   // The teacher's q_k = x_k / X with x_k = exp(u_k - u_max), X their sum (or
@@ -795,11 +845,11 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     const float u0 = a.teacher_lse ? a.teacher_lse[r] : u_max == -INFINITY ? 0.0f : u_max;
     float x_sum = 0.0f, l_sum = 0.0f;
     for (int k = tid; k < K; k += THREADS) {
-      const float ln_x = s_q[k] - u0, x = expf(ln_x);
-      s_q[k] = x;
+      const float ln_x = sl.q[k] - u0, x = expf(ln_x);
+      sl.q[k] = x;
       x_sum += x;
       if (LOSS && !(x == 0.0f))
-        l_sum += x * (ln_x - (empty ? -INFINITY : (s_z[k] - M) * a.inv_t - ln_s));
+        l_sum += x * (ln_x - (empty ? -INFINITY : (sl.z[k] - M) * a.inv_t - ln_s));
     }
     const float2 t = block_add<THREADS>(x_sum, l_sum, sm_add);
     Q = t.x;
@@ -814,7 +864,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
 
   if (GRAD) {
     T* g = static_cast<T*>(a.d_logits) + r * a.grad_stride;
-    const float al = a.d_logprob && target >= 0 ? a.d_logprob[r] : 0.0f;
+    const float al = a.d_logprob && labels.target >= 0 ? a.d_logprob[r] : 0.0f;
     const float w = a.d_loss ? a.d_loss[r] : 0.0f, b = a.d_entropy ? a.d_entropy[r] : 0.0f;
     float A = 0.0f, B = 0.0f, A1 = 0.0f, M1 = M, at_target = 0.0f;
     bool zero;
@@ -858,13 +908,18 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     // The columns of the target and the teacher's ids, from the logits kept
     // above (z may be overwritten by now). Equal ids all store the same value.
     for (int k = tid; k <= K; k += THREADS) {
-      const int32_t id = s_id[k];
+      const int32_t id = sl.id[k];
       if (id < part.lo || id >= part.hi || zero) continue;
       float q = 0.0f;
-      for (int i = 0; i < K; ++i)
-        if (s_id[i] == id) q += s_q[i];
-      float x = smooth<ENTROPY, OWN>(row, {s_z[k], 0.0f}).x - w * a.inv_t * (q * per_x);
-      if (id == target) x += at_target;
+      for (int i = 0; i < K; i += 4) {
+        const int4 ids = *reinterpret_cast<const int4*>(sl.id + i);
+        if (ids.x == id) q += sl.q[i];
+        if (ids.y == id && i + 1 < K) q += sl.q[i + 1];
+        if (ids.z == id && i + 2 < K) q += sl.q[i + 2];
+        if (ids.w == id && i + 3 < K) q += sl.q[i + 3];
+      }
+      float x = smooth<ENTROPY, OWN>(row, {sl.z[k], 0.0f}).x - w * a.inv_t * (q * per_x);
+      if (id == labels.target) x += at_target;
       store(g + id, x);
     }
   }
@@ -906,21 +961,56 @@ RowArgs row_args(const VocabLaunch& in) {
   return a;
 }
 
+// The threads of a row's block. A block's fixed work (labels, joining its
+// threads' sums, the hand-over to the next block: some 3 us) is hidden by the
+// other blocks of its SM, so many rows want small blocks, as long as a thread's
+// share of the row does not outgrow what the SM keeps in flight. By the row's
+// bytes, from sweeps of 32..256 threads over 1000..64000 logits of both types
+// (about 16000 rows, us with 32 / 64 / 128 / 256 threads, bf16):
+//   sums alone      8 KB 25.5 / 29.5 / 41 / 71, 64 KB 84 / 82 / 80 / 87, 300 KB 128: 189, 256: 180
+//   alternatives    4 KB 128 / 90 / 95 / 175, 64 KB 264 / 172 / 139 / 171, 128 KB 128: 123, 256: 130
+//   gradient alone  4 KB 21 / 25 / 39 / 75, 16 KB 81 / 78 / 82 / 100, 64 KB 158 / 154 / 150 / 148
+//   both in one     8 KB 55 / 56 / 77 / 133, 16 KB 105 / 91 / 101 / 152, 32 KB 230 / 186 / 170 / 199,
+//                   64 KB 235 / 224 / 184 / 174
+// Few rows want larger ones, until the SMs are full. The search for the
+// alternatives starts from the threads' best chunks: four for each alternative.
+template <typename T, bool LOSS, bool GRAD, bool TOP>
+int threads_of(const VocabLaunch& in) {
+  const int64_t bytes = in.vocab * (int64_t)sizeof(T), chunks = in.vocab / kPer<T>;
+  const int64_t kb = 1024;
+  int threads;
+  if (TOP)
+    threads = bytes <= 8 * kb ? 64 : bytes <= 80 * kb ? 128 : 256;
+  else if (!GRAD)
+    threads = bytes <= 20 * kb ? 32 : bytes <= 48 * kb ? 64 : bytes <= 256 * kb ? 128 : 256;
+  else if (!LOSS)
+    threads = bytes <= 10 * kb ? 32 : bytes <= 20 * kb ? 64 : 128;
+  else
+    threads = bytes <= 10 * kb ? 32 : bytes <= 20 * kb ? 64 : bytes <= 48 * kb ? 128 : 256;
+  while (threads < kMaxThreads &&
+         ((in.rows * threads < kSMs * kResident && chunks >= 2 * threads) ||
+          (TOP && threads < 4 * in.top_k)))
+    threads *= 2;
+  return threads;
+}
+
 // How many blocks share a row (1, 2, 4 or 8; a cluster when they must meet).
-//  - Few rows: until the blocks fill the GPU (the gradient alone: four times
-//    over), as long as every thread has a chunk.
+//  - Few rows: until every SM has a block (the gradient alone, whose blocks need
+//    not meet: 16), as long as every thread has a chunk.
 //  - Loss and gradient in one call: the rows in flight are read twice, so they
-//    are to stay in L2.
+//    are to stay in L2 (8192 x 151936 bf16: 1063 us with one block, 966 with
+//    two, 993 with four).
 //  - Top alternatives: the table of a block's part stays under a quarter of an
 //    SM's shared memory.
 template <typename T, bool LOSS, bool GRAD, bool TOP>
-int split_of(const VocabLaunch& in) {
-  const int64_t chunks = in.vocab / kPer<T>;
-  const int64_t blocks = kSMs * (kResident / kLong), fill = LOSS ? blocks : 4 * blocks;
+int split_of(const VocabLaunch& in, int threads) {
+  const int64_t chunks = in.vocab / kPer<T>, blocks = kSMs * (kResident / threads);
+  const int64_t fill = LOSS ? kSMs : 16 * kSMs;
   int split = 1;
-  while (split < kMaxSplit && in.rows * split < fill && chunks >= 2 * split * kLong) split *= 2;
+  while (split < kMaxSplit && in.rows * split < fill && chunks >= 2 * split * threads) split *= 2;
   if (LOSS && GRAD)
-    while (split < kMaxSplit && blocks / split * in.vocab * (int64_t)sizeof(T) > kRowsInL2) split *= 2;
+    while (split < kMaxSplit && blocks / split * in.vocab * (int64_t)sizeof(T) > kRowsInL2)
+      split *= 2;
   if (TOP)
     while (split < kMaxSplit && chunks / split * (int64_t)sizeof(T) > kTableBytes) split *= 2;
   return split;
@@ -935,7 +1025,7 @@ cudaError_t launch_rows(const VocabLaunch& in, int split, cudaStream_t stream) {
   size_t smem = 0;
   if (TOP) {
     // The table: an entry for each 32 bytes of the part, and two ends.
-    smem = sizeof(TopShared) + (in.vocab < kListed ? in.vocab : kListed) * 8 +
+    smem = sizeof(TopShared) + list_capacity(in.top_k) * 8 +
            (in.vocab / kPer<T> / split + 4) * sizeof(T);
     static std::atomic<bool> allowed[64];
     int dev = 0;
@@ -953,10 +1043,15 @@ cudaError_t launch_rows(const VocabLaunch& in, int split, cudaStream_t stream) {
 
 template <typename T, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
 cudaError_t launch_typed(const VocabLaunch& in, cudaStream_t stream) {
-  if (in.vocab / kPer<T> <= kShortChunks)
-    return launch_rows<T, kShort, LOSS, GRAD, ENTROPY, OWN, TOP>(in, 1, stream);
-  return launch_rows<T, kLong, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split_of<T, LOSS, GRAD, TOP>(in),
-                                                              stream);
+  const int threads = threads_of<T, LOSS, GRAD, TOP>(in);
+  const int split = split_of<T, LOSS, GRAD, TOP>(in, threads);
+  if (threads == 256)
+    return launch_rows<T, 256, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split, stream);
+  if (threads == 128)
+    return launch_rows<T, 128, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split, stream);
+  if (TOP || threads == 64)
+    return launch_rows<T, 64, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split, stream);
+  return launch_rows<T, TOP ? 64 : 32, LOSS, GRAD, ENTROPY, OWN, TOP>(in, split, stream);
 }
 
 template <bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
