@@ -353,13 +353,25 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     __syncthreads();  // total_of's last answer has been read
     if (tid == 0) sh.count = sh.total = 0;
     __syncthreads();
+    // (NaN where the bound is 0 or a NaN's key: nothing compares below it)
     const float at_least = key_value<T>(bound);
-    for (int p = tid; look && p < ch.count(); p += THREADS) {
-      if (value_of(ch.maxima[p]) < at_least) continue;
-      const uint64_t key = ch.key(p);
-      if (key < bound || key == 0) continue;
-      const int at = atomicAdd(&sh.total, 1);
-      if (at < kFound) sh.found[at] = p;
+    for (int p0 = tid; look && p0 < ch.count(); p0 += 32 * THREADS) {
+      uint32_t reach = 0;
+      for (int i = 0; i < 32; ++i) {
+        const int p = p0 + i * THREADS;
+        if (p >= ch.count()) break;
+        const float most = value_of(ch.maxima[p]);
+        if (most < at_least) continue;
+        if (most == at_least || p >= ch.sp.body) {
+          const uint64_t key = ch.key(p);
+          if (key < bound || key == 0) continue;
+        }
+        reach |= 1u << i;
+      }
+      if (reach == 0) continue;
+      int at = atomicAdd(&sh.total, __popc(reach));
+      for (; reach != 0 && at < kFound; reach &= reach - 1, ++at)
+        sh.found[at] = p0 + (__ffs(reach) - 1) * THREADS;
     }
     __syncthreads();
     if (sh.total > kFound) return sh.capacity + 1;
@@ -381,10 +393,13 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
 #pragma unroll
         for (int i = 0; i < kPer<T>; ++i) x[i] = lo + i < hi ? value_of(z[lo + i]) : 0.0f;
       }
+      // Elements equal to the bound's value reach it if their chunk's place does.
+      const bool equal = rank_key<T>(at_least, ch.position(p)) >= bound;
       uint32_t reach = 0;
 #pragma unroll
       for (int i = 0; i < kPer<T>; ++i)
-        if (lo + i < hi && rank_key<T>(x[i], ch.position(p)) >= bound) reach |= 1u << i;
+        if (!(equal ? x[i] < at_least : x[i] <= at_least)) reach |= 1u << i;
+      reach &= (1u << (hi - lo)) - 1u;
       int at = atomicAdd(&sh.count, __popc(reach));
 #pragma unroll
       for (int i = 0; i < kPer<T>; ++i)
@@ -421,6 +436,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     const uint64_t key = sh.list[i];
     if (key < bound) continue;
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += sh.list[j] > key;
     if (rank < k) sh.best[rank] = key;
   }
@@ -973,7 +989,7 @@ RowArgs row_args(const VocabLaunch& in) {
 //   both in one     8 KB 55 / 56 / 77 / 133, 16 KB 105 / 91 / 101 / 152, 32 KB 230 / 186 / 170 / 199,
 //                   64 KB 235 / 224 / 184 / 174
 // Few rows want larger ones, until the SMs are full. The search for the
-// alternatives starts from the threads' best chunks: four for each alternative.
+// alternatives starts from the threads' best chunks: three for each alternative.
 template <typename T, bool LOSS, bool GRAD, bool TOP>
 int threads_of(const VocabLaunch& in) {
   const int64_t bytes = in.vocab * (int64_t)sizeof(T), chunks = in.vocab / kPer<T>;
@@ -983,13 +999,11 @@ int threads_of(const VocabLaunch& in) {
     threads = bytes <= 8 * kb ? 64 : bytes <= 80 * kb ? 128 : 256;
   else if (!GRAD)
     threads = bytes <= 20 * kb ? 32 : bytes <= 48 * kb ? 64 : bytes <= 256 * kb ? 128 : 256;
-  else if (!LOSS)
-    threads = bytes <= 10 * kb ? 32 : bytes <= 20 * kb ? 64 : 128;
   else
     threads = bytes <= 10 * kb ? 32 : bytes <= 20 * kb ? 64 : bytes <= 48 * kb ? 128 : 256;
   while (threads < kMaxThreads &&
          ((in.rows * threads < kSMs * kResident && chunks >= 2 * threads) ||
-          (TOP && threads < 4 * in.top_k)))
+          (TOP && threads < 3 * in.top_k)))
     threads *= 2;
   return threads;
 }
