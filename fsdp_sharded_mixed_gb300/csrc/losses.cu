@@ -609,9 +609,10 @@ __device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// Writes the smooth part of the gradient of a block's part of a row. Each element is read and written
-// by one thread, so g may be z. Rows of z and g that sit differently in their
-// 32-byte chunks (other strides or bases) go element by element.
+// Writes the smooth part of the gradient of a block's part of a row. Each
+// element is read and written by one thread, so g may be z. Rows of z and g
+// that sit differently in their 32-byte chunks (other strides or bases) go
+// element by element.
 template <typename T, int THREADS, bool ENTROPY, bool OWN>
 __device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, const GradRow& r,
                                            unsigned int* err) {
@@ -667,7 +668,7 @@ __device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, con
   }
 }
 
-// The block's sums of x and y (and of u's largest); every thread gets them.
+// The block's sums of x and y; every thread gets them.
 template <int THREADS>
 __device__ __forceinline__ float2 block_add(float x, float y, float2* sm) {
   for (int off = 16; off > 0; off >>= 1) {
@@ -694,10 +695,10 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, uint32_t bits) 
   return __uint_as_float(a.teacher_bf16 ? bits << 16 : bits);
 }
 
-// A row's labels: the target (-1: none), and the teacher's record with the
-// logits of its columns. The loads of thread k's entry are issued, and waited
-// for, in three steps between which the block does other work; a record longer
-// than the block is read in the last one.
+// A row's labels: the target (-1: none), the teacher's record with the logits
+// of its columns, the upstream gradients and normalisers. The loads of thread
+// k's entry are issued, and waited for, in three steps between which the block
+// does other work; a record longer than the block is read in the last one.
 struct LabelsShared {
   int32_t id[ZS_MAX_TEACHER + 4];  // the teacher's ids and the target, then -1 up to a multiple of 4
   float q[ZS_MAX_TEACHER];         // u = t / T (-inf: unused), then x_k = exp(u - u_max)
@@ -715,6 +716,8 @@ struct Labels {
   int64_t raw_target = -1;
   uint32_t my_t = 0;
   float my_z = 0.0f, z_target = 0.0f;
+  float w = 0.0f, al = 0.0f, b = 0.0f;  // d_loss, d_logprob, d_entropy
+  float teacher_lse = 0.0f, lse = 0.0f, hard_lse = 0.0f, entropy = 0.0f;
   bool bad_target = false;
 
   // Whether this block needs the logit of a column: for the losses, or because
@@ -741,6 +744,17 @@ struct Labels {
       my_t = teacher_bits(a, r * a.teacher_k + k);
     }
     if (a.targets) raw_target = a.targets[r];
+    if (teacher && a.teacher_lse) teacher_lse = a.teacher_lse[r];
+    if (GRAD) {
+      if (a.d_loss) w = a.d_loss[r];
+      if (a.d_logprob) al = a.d_logprob[r];
+      if (!LOSS) {
+        if (a.d_entropy) b = a.d_entropy[r];
+        if (a.in_lse) lse = a.in_lse[r];
+        if (a.in_hard_lse) hard_lse = a.in_hard_lse[r];
+        if (a.in_entropy) entropy = a.in_entropy[r];
+      }
+    }
   }
   __device__ __forceinline__ void gather() {
     my_id = checked(my_id);
@@ -749,6 +763,7 @@ struct Labels {
     if (bad_target && first && threadIdx.x == 0) atomicOr(a.err, 1u);
     if (raw_target >= 0 && !bad_target) target = (int32_t)raw_target;
     if (wanted(target)) z_target = value_of(z[target]);
+    if (target < 0) al = 0.0f;
   }
   __device__ __forceinline__ float finish() {
     const int K = a.teacher_k, tid = threadIdx.x;
@@ -858,7 +873,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
   //   sum_k q_k (ln q_k - ln p_k) = (1/X) sum_k x_k (ln x_k - ln p_k) - Q ln X.
   float Q = 0.0f, per_x = 1.0f;
   if (teacher) {
-    const float u0 = a.teacher_lse ? a.teacher_lse[r] : u_max == -INFINITY ? 0.0f : u_max;
+    const float u0 = a.teacher_lse ? labels.teacher_lse : u_max == -INFINITY ? 0.0f : u_max;
     float x_sum = 0.0f, l_sum = 0.0f;
     for (int k = tid; k < K; k += THREADS) {
       const float ln_x = sl.q[k] - u0, x = expf(ln_x);
@@ -880,8 +895,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
 
   if (GRAD) {
     T* g = static_cast<T*>(a.d_logits) + r * a.grad_stride;
-    const float al = a.d_logprob && labels.target >= 0 ? a.d_logprob[r] : 0.0f;
-    const float w = a.d_loss ? a.d_loss[r] : 0.0f, b = a.d_entropy ? a.d_entropy[r] : 0.0f;
+    const float al = labels.al, w = labels.w, b = labels.b;
     float A = 0.0f, B = 0.0f, A1 = 0.0f, M1 = M, at_target = 0.0f;
     bool zero;
     if (LOSS) {
@@ -893,8 +907,8 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
         A -= al / S;
       at_target = al;
     } else if (a.distill) {
-      if (a.in_hard_lse) lse = lse1 = a.in_hard_lse[r];
-      if (a.in_lse) lse = a.in_lse[r];
+      if (a.in_hard_lse) lse = lse1 = labels.hard_lse;
+      if (a.in_lse) lse = labels.lse;
       zero = lse == -INFINITY;
       M = lse / a.inv_t;
       M1 = lse1;
@@ -905,10 +919,10 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
         A -= al;
       at_target = al;
     } else {
-      lse = a.in_lse[r];
+      lse = labels.lse;
       zero = lse == -INFINITY;
       M = lse / a.inv_t;
-      A = -(al + (b == 0.0f ? 0.0f : b * a.in_entropy[r])) * a.inv_t;
+      A = -(al + (b == 0.0f ? 0.0f : b * labels.entropy)) * a.inv_t;
       B = -b * kLn2 * a.inv_t;
       at_target = al * a.inv_t;
     }
