@@ -14,6 +14,16 @@
 //
 // z - M is formed before the scaling: both may be the type's lowest value (a
 // row masked with it), whose product with 1/T is no longer finite.
+//
+// Bound: HBM. A call reads its logits once (V * 2 or 4 bytes a row) and, with
+// a gradient, writes as much; 6 to 15 flops and one or two exponentials an
+// element. On GB300, as a share of the measured copy bandwidth (6779 GB/s):
+// scoring 4096 x 151936 bf16 180.5 us = 1.02; evaluating 8192 x 32000 bf16, T = 2
+// with hard labels, 86 us = 0.91; the gradient alone of 8192 x 50257 bf16 235 us =
+// 1.00; loss and gradient in one call 0.82 (4095 x 32000, 94.4 us) and 0.76
+// (8192 x 151936, 965 us), where a block's reading and writing take turns; 64
+// alternatives of 8191 x 32000 fp32 220 us = 0.71, the search coming after the
+// stream. Small calls take 3 to 9 us of GPU time, less than a call from Python.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -32,10 +42,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxThreads = 256;         // of a row's block (32, 64, 128 or 256)
 constexpr int kResident = 1024;          // threads of an SM: 64 registers each
 constexpr int kSMs = 152;
-constexpr int kMaxSplit = 8;               // blocks of a row: the portable cluster size
-constexpr int64_t kRowsInL2 = 96 << 20;   // bytes of rows in flight that L2 (129 MB) keeps
+constexpr int kMaxSplit = 8;             // blocks of a row: the portable cluster size
+constexpr int64_t kRowsInL2 = 96 << 20;  // bytes of rows in flight that L2 (129 MB) keeps
 constexpr int64_t kTableBytes = 40 << 10;
-constexpr int kMaxSmem = 200 * 1024;      // dynamic shared memory of a block
+constexpr int kMaxSmem = 200 * 1024;     // dynamic shared memory of a block
 
 struct RowArgs {
   const void* logits;
@@ -215,8 +225,7 @@ __device__ __forceinline__ Sums moved(const Sums& a, float M, float scale) {
   return {M, f * a.s, f * fmaf(a.s, delta, a.u), f1 * a.s1};
 }
 
-// The block's sums, in a fixed order, and the largest of its u; every thread
-// gets them.
+// What a block's warps share to join their sums and their largest u.
 struct BlockSums {
   Sums sums[kMaxThreads / 32];
   float u[kMaxThreads / 32];
@@ -238,6 +247,7 @@ __device__ __forceinline__ float lane_max(float x, int n) {
   for (int off = n / 2; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
   return x;
 }
+// The block's sums, in a fixed order, and its largest u; every thread gets them.
 template <int THREADS, bool ENTROPY, bool OWN>
 __device__ __forceinline__ Sums block_sums(Sums t, float scale, float* u, BlockSums& sm) {
   constexpr int kWarps = THREADS / 32;
@@ -266,6 +276,7 @@ __device__ __forceinline__ uint64_t rank_key(float z, int32_t position) {
   return ((uint64_t)u << 32) | (uint32_t)~position;
 }
 
+// The value of a key (NaN for a NaN's and for key 0).
 template <typename T>
 __device__ __forceinline__ float key_value(uint64_t key) {
   const uint32_t u = (uint32_t)(key >> 32);
@@ -282,6 +293,7 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 // Table entry p: body chunk p; then the tail and the head (whose position comes
 // first). An end without elements has key 0. Entry p belongs to thread p modulo
 // the block.
+
 // Elements that may be ranked: those of k chunks at least, and enough for the
 // sorted lists of a row's blocks.
 __host__ __device__ __forceinline__ int list_capacity(int k) { return 16 * (k < 16 ? 16 : k); }
@@ -444,8 +456,9 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
 }
 
 // The sums of a block's part of a row: each thread keeps kFlight chunks in
-// flight ahead of those that it works on. TOP: the table, and the thread's best
-// chunk.
+// flight ahead of those that it works on (four single ones in turn, the same
+// registers, took 238 us instead of 180 for 4096 x 151936 bf16). TOP: the table,
+// and the thread's best chunk.
 constexpr int kFlight = 2;
 // labels: its read() asks for a row's labels once the first chunks are on their
 // way, gather() for the logits that they name after the first of them were used,
@@ -504,8 +517,8 @@ __device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scal
   }
   if (sp.body == 0) labels.gather();
   *u = labels.finish();
-  return block_sums<THREADS, ENTROPY, OWN>({st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale,
-                             u, sm);
+  return block_sums<THREADS, ENTROPY, OWN>(
+      {st.m, st.s.x + st.s.y, st.u.x + st.u.y, st.s1.x + st.s1.y}, scale, u, sm);
 }
 
 // ---- the blocks of a row ----------------------------------------------------------
@@ -604,8 +617,9 @@ __device__ __forceinline__ void put_pair(uint32_t* w, int i, float2 g, float) {
 }
 // (a gradient is not read again soon)
 __device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
-  asm volatile("st.global.L2::evict_first.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+  asm volatile("st.global.L2::evict_first.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+               "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+               "r"(w[7])
                : "memory");
 }
 
@@ -700,7 +714,7 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, uint32_t bits) 
 // k's entry are issued, and waited for, in three steps between which the block
 // does other work; a record longer than the block is read in the last one.
 struct LabelsShared {
-  int32_t id[ZS_MAX_TEACHER + 4];  // the teacher's ids and the target, then -1 up to a multiple of 4
+  int32_t id[ZS_MAX_TEACHER + 4];  // the teacher's ids, the target, -1 up to a multiple of 4
   float q[ZS_MAX_TEACHER];         // u = t / T (-inf: unused), then x_k = exp(u - u_max)
   float z[ZS_MAX_TEACHER + 1];
 };
@@ -783,9 +797,16 @@ struct Labels {
   }
 };
 
-// A row per block, or per cluster of a.split blocks (LOSS) or a.split
-// independent blocks (the gradient alone). LOSS: statistics and losses from the
-// logits; GRAD: the gradient, from them or from the forward call's normalisers.
+// A row per block, or per cluster of 2^shift blocks (LOSS) or as many independent
+// ones (the gradient alone). LOSS: statistics and losses from the logits; GRAD:
+// the gradient, from them or from the forward call's normalisers. The row is
+// streamed by all threads; what else it takes is kept off that stream: labels
+// are asked for behind its first loads, the blocks of an SM are at different
+// points of their rows, the next kernel's are placed as the last rows retire.
+// Of the 14.5 thousand cycles (7.6 us) of a 32000-logit bf16 row in a block of 256
+// threads the stream was 10; a block of 128 spends the same on the rest of a row
+// that it streams twice as long, with twice as many beside it (98 -> 86 us for
+// 8192 rows).
 template <typename T, int THREADS, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
 __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     rows_kernel(const __grid_constant__ RowArgs a) {
@@ -997,11 +1018,13 @@ RowArgs row_args(const VocabLaunch& in) {
 // share of the row does not outgrow what the SM keeps in flight. By the row's
 // bytes, from sweeps of 32..256 threads over 1000..64000 logits of both types
 // (about 16000 rows, us with 32 / 64 / 128 / 256 threads, bf16):
-//   sums alone      8 KB 25.5 / 29.5 / 41 / 71, 64 KB 84 / 82 / 80 / 87, 300 KB 128: 189, 256: 180
-//   alternatives    4 KB 128 / 90 / 95 / 175, 64 KB 264 / 172 / 139 / 171, 128 KB 128: 123, 256: 130
+//   sums alone      8 KB 25.5 / 29.5 / 41 / 71, 64 KB 84 / 82 / 80 / 87,
+//                   300 KB (4096 rows) - / - / 189 / 180
+//   alternatives    4 KB 128 / 90 / 95 / 175, 64 KB 264 / 172 / 139 / 171,
+//                   128 KB - / - / 123 / 130
 //   gradient alone  4 KB 21 / 25 / 39 / 75, 16 KB 81 / 78 / 82 / 100, 64 KB 158 / 154 / 150 / 148
-//   both in one     8 KB 55 / 56 / 77 / 133, 16 KB 105 / 91 / 101 / 152, 32 KB 230 / 186 / 170 / 199,
-//                   64 KB 235 / 224 / 184 / 174
+//   both in one     8 KB 55 / 56 / 77 / 133, 16 KB 105 / 91 / 101 / 152,
+//                   32 KB 230 / 186 / 170 / 199, 64 KB 235 / 224 / 184 / 174
 // Few rows want larger ones, until the SMs are full. The search for the
 // alternatives starts from the threads' best chunks: three for each alternative.
 template <typename T, bool LOSS, bool GRAD, bool TOP>

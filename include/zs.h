@@ -568,7 +568,8 @@ zs_status zs_distill_loss_grad(const void* logits, zs_dtype dtype, int64_t rows,
 const char* zs_status_string(zs_status status);
 const char* zs_last_error(void);
 /* Synchronises `cuda_stream`, then reads and clears this device's error word
- * (set by the bounds-checked build's checks and by bounded waits);
+ * (set by the bounds-checked build's checks, by bounded waits, and by token ids
+ * outside the vocabulary);
  * ZS_ERR_TIMEOUT or ZS_ERR_RANGE if it was set, ZS_ERR_CUDA if the stream
  * reports an error. The library looks the addresses of its device arrays
  * (this error word, the no-alloc norm scratch) up once per device and keeps
