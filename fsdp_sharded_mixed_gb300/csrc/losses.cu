@@ -623,13 +623,25 @@ __device__ __forceinline__ void store_chunk(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// Writes the smooth part of the gradient of a block's part of a row. Each
+// The chunks of a part that start at the q0-th, kFlight of them a thread.
+template <typename T, int THREADS>
+__device__ __forceinline__ void load_ahead(uint32_t (&w)[kFlight][kWords], const T* z,
+                                           const Part& sp, int q0, unsigned int* err) {
+#pragma unroll
+  for (int f = 0; f < kFlight; ++f) {
+    const int q = q0 + f * THREADS + threadIdx.x;
+    const int64_t at = sp.lo + sp.head + (int64_t)q * kPer<T>;
+    if (q < sp.body && within(at, at + kPer<T>, sp.lo, sp.hi, err)) load_chunk<kOnce>(w[f], z + at);
+  }
+}
+// Writes the smooth part of the gradient of a block's part of a row, whose first
+// chunks load_ahead has asked for. Each
 // element is read and written by one thread, so g may be z. Rows of z and g
 // that sit differently in their 32-byte chunks (other strides or bases) go
 // element by element.
 template <typename T, int THREADS, bool ENTROPY, bool OWN>
-__device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, const GradRow& r,
-                                           unsigned int* err) {
+__device__ __forceinline__ void write_part(uint32_t (&now)[kFlight][kWords], const T* z, T* g,
+                                           const Part& sp, const GradRow& r, unsigned int* err) {
   const int tid = threadIdx.x;
   if (((uintptr_t)z ^ (uintptr_t)g) % kChunkBytes != 0) {
 #pragma unroll 4
@@ -642,13 +654,12 @@ __device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, con
   };
   if (tid < sp.head) one(tid);
   if (tid < sp.tail) one(sp.hi - sp.tail + tid);
-  const T* zb = z + sp.lo + sp.head;
   T* gb = g + sp.lo + sp.head;
   auto in_row = [&](int q) {
     const int64_t at = sp.lo + sp.head + (int64_t)q * kPer<T>;
     return q < sp.body && within(at, at + kPer<T>, sp.lo, sp.hi, err);
   };
-  uint32_t now[kFlight][kWords], next[kFlight][kWords], out[kWords];
+  uint32_t next[kFlight][kWords], out[kWords];
   if (r.zero) {  // not read at all: it may hold anything
 #pragma unroll
     for (int i = 0; i < kWords; ++i) out[i] = 0;
@@ -656,16 +667,8 @@ __device__ __forceinline__ void write_part(const T* z, T* g, const Part& sp, con
       if (in_row(q)) store_chunk(gb + (int64_t)q * kPer<T>, out);
     return;
   }
-  auto load = [&](uint32_t(*w)[kWords], int q0) {
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int q = q0 + f * THREADS + tid;
-      if (in_row(q)) load_chunk<kOnce>(w[f], zb + (int64_t)q * kPer<T>);
-    }
-  };
-  load(now, 0);
   for (int q0 = 0; q0 < sp.body; q0 += kFlight * THREADS) {
-    load(next, q0 + kFlight * THREADS);
+    load_ahead<T, THREADS>(next, z, sp, q0 + kFlight * THREADS, err);
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       const int q = q0 + f * THREADS + tid;
@@ -715,7 +718,7 @@ __device__ __forceinline__ float teacher_logit(const RowArgs& a, uint32_t bits) 
 // does other work; a record longer than the block is read in the last one.
 struct LabelsShared {
   int32_t id[ZS_MAX_TEACHER + 4];  // the teacher's ids, the target, -1 up to a multiple of 4
-  float q[ZS_MAX_TEACHER];         // u = t / T (-inf: unused), then x_k = exp(u - u_max)
+  float q[ZS_MAX_TEACHER + 4];     // u = t / T (-inf: unused), then x_k = exp(u - u_max); 0
   float z[ZS_MAX_TEACHER + 1];
 };
 template <typename T, int THREADS, bool LOSS, bool GRAD>
@@ -729,7 +732,7 @@ struct Labels {
   int32_t my_id = -1, target = -1;
   int64_t raw_target = -1;
   uint32_t my_t = 0;
-  float my_z = 0.0f, z_target = 0.0f;
+  T my_z = T(0.0f), z_target = T(0.0f);  // (as stored: a conversion would wait for them)
   float w = 0.0f, al = 0.0f, b = 0.0f;  // d_loss, d_logprob, d_entropy
   float teacher_lse = 0.0f, lse = 0.0f, hard_lse = 0.0f, entropy = 0.0f;
   bool bad_target = false;
@@ -772,18 +775,18 @@ struct Labels {
   }
   __device__ __forceinline__ void gather() {
     my_id = checked(my_id);
-    if (wanted(my_id)) my_z = value_of(z[my_id]);
+    if (wanted(my_id)) my_z = z[my_id];
     bad_target = raw_target >= a.vocab;
     if (bad_target && first && threadIdx.x == 0) atomicOr(a.err, 1u);
     if (raw_target >= 0 && !bad_target) target = (int32_t)raw_target;
-    if (wanted(target)) z_target = value_of(z[target]);
+    if (wanted(target)) z_target = z[target];
     if (target < 0) al = 0.0f;
   }
   __device__ __forceinline__ float finish() {
     const int K = a.teacher_k, tid = threadIdx.x;
     float u = -INFINITY;
     if (teacher) {
-      if (tid < K) put(tid, my_id, my_t, my_z, &u);
+      if (tid < K) put(tid, my_id, my_t, value_of(my_z), &u);
       for (int k = tid + THREADS; k < K; k += THREADS) {
         const int32_t id = checked(a.teacher_ids[r * K + k]);
         put(k, id, teacher_bits(a, r * K + k), wanted(id) ? value_of(z[id]) : 0.0f, &u);
@@ -791,7 +794,8 @@ struct Labels {
     }
     if (GRAD && tid < 4) {
       sh.id[K + tid] = tid == 0 ? target : -1;
-      if (tid == 0) sh.z[K] = z_target;
+      sh.q[K + tid] = 0.0f;
+      if (tid == 0) sh.z[K] = value_of(z_target);
     }
     return u;
   }
@@ -824,6 +828,10 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
   __shared__ __align__(16) LabelsShared sl;
   Labels<T, THREADS, LOSS, GRAD> labels = {a, z, r, part, first, teacher, sl};
   float u_max = -INFINITY;
+  // GRAD: the first chunks; for the gradient alone they are on their way while
+  // the row's constants are made. (After the sums that early a load costs more in
+  // registers than it hides: 4095 x 32000 94.5 against 95.1 us.)
+  uint32_t ahead[kFlight][kWords];
 
   float M = 0.0f, S = 1.0f, S1 = 1.0f, lse = 0.0f, lse1 = 0.0f, ln_s = 0.0f;
   bool empty = false;
@@ -871,7 +879,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
         a.logprob[r] = labels.bad_target   ? NAN
                        : labels.target < 0 ? 0.0f
                        : empty             ? -INFINITY
-                                           : (labels.z_target - M) * t - (a.distill ? ln_s1 : ln_s);
+                                           : (value_of(labels.z_target) - M) * t - (a.distill ? ln_s1 : ln_s);
       }
     }
     if (TOP && first) {
@@ -884,6 +892,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     }
   } else {
     labels.read();
+    load_ahead<T, THREADS>(ahead, z, part, 0, a.err);
     labels.gather();
     u_max = labels.finish();
     block_sums<THREADS, false, false>({0.0f, 0.0f, 0.0f, 0.0f}, 0.0f, &u_max, sm_sums);
@@ -954,7 +963,8 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     if (A1 == 0.0f) M1 = INFINITY;
     const GradRow row = {A, B, A1, M, M1, a.scale, zero};
     __syncthreads();  // the labels, before anything is overwritten in place
-    write_part<T, THREADS, ENTROPY, OWN>(z, g, part, row, a.err);
+    if (LOSS) load_ahead<T, THREADS>(ahead, z, part, 0, a.err);
+    write_part<T, THREADS, ENTROPY, OWN>(ahead, z, g, part, row, a.err);
     __syncthreads();
     // The columns of the target and the teacher's ids, from the logits kept
     // above (z may be overwritten by now). Equal ids all store the same value.
@@ -962,12 +972,14 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
       const int32_t id = sl.id[k];
       if (id < part.lo || id >= part.hi || zero) continue;
       float q = 0.0f;
+#pragma unroll 4
       for (int i = 0; i < K; i += 4) {
         const int4 ids = *reinterpret_cast<const int4*>(sl.id + i);
-        if (ids.x == id) q += sl.q[i];
-        if (ids.y == id && i + 1 < K) q += sl.q[i + 1];
-        if (ids.z == id && i + 2 < K) q += sl.q[i + 2];
-        if (ids.w == id && i + 3 < K) q += sl.q[i + 3];
+        const float4 x = *reinterpret_cast<const float4*>(sl.q + i);
+        q += ids.x == id ? x.x : 0.0f;
+        q += ids.y == id ? x.y : 0.0f;
+        q += ids.z == id ? x.z : 0.0f;
+        q += ids.w == id ? x.w : 0.0f;
       }
       float x = smooth<ENTROPY, OWN>(row, {sl.z[k], 0.0f}).x - w * a.inv_t * (q * per_x);
       if (id == labels.target) x += at_target;
@@ -1065,6 +1077,27 @@ int split_of(const VocabLaunch& in, int threads) {
   if (TOP)
     while (split < kMaxSplit && chunks / split * (int64_t)sizeof(T) > kTableBytes) split *= 2;
   return split;
+}
+
+// launch_kernel's launch, in clusters of `cluster` blocks (1: no clusters).
+cudaError_t launch_clusters(int cluster, void (*kernel)(RowArgs), dim3 grid, dim3 block,
+                            size_t smem, cudaStream_t stream, const RowArgs& a) {
+  if (cluster == 1) return launch_kernel(kernel, grid, block, smem, stream, a);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = launch_overlap() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename T, int THREADS, bool LOSS, bool GRAD, bool ENTROPY, bool OWN, bool TOP>
