@@ -359,7 +359,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     return sh.total;
   };
   // Lists the elements at or above the bound: first the chunks that reach it,
-  // then one thread reads each of them again, so that all their loads are in
+  // then their elements, read again by all threads, so that these loads are in
   // flight together. More than fit are counted, not listed.
   auto list_from = [&](uint64_t bound, bool look) {
     __syncthreads();  // total_of's last answer has been read
@@ -369,6 +369,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     const float at_least = key_value<T>(bound);
     for (int p0 = tid; look && p0 < ch.count(); p0 += 32 * THREADS) {
       uint32_t reach = 0;
+#pragma unroll 4
       for (int i = 0; i < 32; ++i) {
         const int p = p0 + i * THREADS;
         if (p >= ch.count()) break;
@@ -387,38 +388,31 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     }
     __syncthreads();
     if (sh.total > kFound) return sh.capacity + 1;
-    for (int f = tid; f < sh.total; f += THREADS) {
-      const int p = sh.found[f];
-      int lo, hi;
-      ch.elements(p, &lo, &hi);
-      if (!within(lo, hi, ch.sp.lo, ch.sp.hi, err)) continue;
-      float x[kPer<T>];
-      if (p < ch.sp.body) {
-        uint32_t w[kWords];
-        load_chunk<kUsual>(w, z + lo);
+    // An element a thread, four of them on their way at once.
+    const int found = sh.total * kPer<T>;
+    for (int i0 = tid; i0 < found; i0 += 4 * THREADS) {
+      float x[4];
+      int place[4], column[4];
 #pragma unroll
-        for (int i = 0; i < kPer<T> / 2; ++i) {
-          x[2 * i] = pair_of(w, i, T()).x;
-          x[2 * i + 1] = pair_of(w, i, T()).y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPer<T>; ++i) x[i] = lo + i < hi ? value_of(z[lo + i]) : 0.0f;
+      for (int f = 0; f < 4; ++f) {
+        const int i = i0 + f * THREADS;
+        column[f] = -1;
+        if (i >= found) continue;
+        const int p = sh.found[i / kPer<T>];
+        int lo, hi;
+        ch.elements(p, &lo, &hi);
+        const int j = lo + i % kPer<T>;
+        if (j >= hi || !within(j, j + 1, ch.sp.lo, ch.sp.hi, err)) continue;
+        x[f] = value_of(z[j]);
+        place[f] = ch.position(p);
+        column[f] = j;
       }
-      // Elements equal to the bound's value reach it if their chunk's place does.
-      const bool equal = rank_key<T>(at_least, ch.position(p)) >= bound;
-      uint32_t reach = 0;
 #pragma unroll
-      for (int i = 0; i < kPer<T>; ++i)
-        if (!(equal ? x[i] < at_least : x[i] <= at_least)) reach |= 1u << i;
-      reach &= (1u << (hi - lo)) - 1u;
-      int at = atomicAdd(&sh.count, __popc(reach));
-#pragma unroll
-      for (int i = 0; i < kPer<T>; ++i)
-        if (reach >> i & 1) {
-          if (at < sh.capacity) sh.list[at] = rank_key<T>(x[i], lo + i);
-          ++at;
-        }
+      for (int f = 0; f < 4; ++f) {
+        if (column[f] < 0 || rank_key<T>(x[f], place[f]) < bound) continue;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < sh.capacity) sh.list[at] = rank_key<T>(x[f], column[f]);
+      }
     }
     __syncthreads();
     return sh.count;
