@@ -18,12 +18,12 @@
 // Bound: HBM. A call reads its logits once (V * 2 or 4 bytes a row) and, with
 // a gradient, writes as much; 6 to 15 flops and one or two exponentials an
 // element. On GB300, as a share of the measured copy bandwidth (6779 GB/s):
-// scoring 4096 x 151936 bf16 180.5 us = 1.02; evaluating 8192 x 32000 bf16, T = 2
-// with hard labels, 86 us = 0.91; the gradient alone of 8192 x 50257 bf16 235 us =
-// 1.00; loss and gradient in one call 0.82 (4095 x 32000, 94.4 us) and 0.76
-// (8192 x 151936, 965 us), where a block's reading and writing take turns; 64
-// alternatives of 8191 x 32000 fp32 220 us = 0.71, the search coming after the
-// stream. Small calls take 3 to 9 us of GPU time, less than a call from Python.
+// scoring 4096 x 151936 bf16 178 us = 1.03; evaluating 8192 x 32000 bf16, T = 2
+// with hard labels, 85.4 us = 0.91; the gradient alone of 8192 x 50257 bf16 237 us
+// = 0.99; loss and gradient in one call 0.87 (4095 x 32000, 89.0 us) and 0.76
+// (8192 x 151936, 963 us), where a block's reading and writing take turns; 64
+// alternatives of 8191 x 32000 fp32 218 us = 0.71, the search coming after the
+// stream. Small calls take 3 to 8 us of GPU time, less than a call from Python.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -450,7 +450,9 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
 }
 
 // The sums of a block's part of a row: each thread keeps kFlight chunks in
-// flight ahead of those that it works on (four single ones in turn, the same
+// flight ahead of those that it works on, two sets of buffers taking turns (one
+// copied to the other: 92 instead of 89 us for loss and gradient of 4095 x 32000
+// bf16; four single ones in turn, the same
 // registers, took 238 us instead of 180 for 4096 x 151936 bf16). TOP: the table,
 // and the thread's best chunk.
 constexpr int kFlight = 2;
@@ -491,23 +493,26 @@ __device__ __forceinline__ Sums part_sums(const T* z, const Part& sp, float scal
       store(maxima + sp.body + 1, h);
     }
   }
-  for (int q0 = 0; q0 < sp.body; q0 += kFlight * THREADS) {
-    load(next, q0 + kFlight * THREADS);
+  auto use = [&](uint32_t(*w)[kWords], int q0) {
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f)
-      if (q0 + f * THREADS + tid < sp.body) {
-        const float cm = st.template add_chunk<T>(now[f], scale, slack);
-        if (TOP) {
-          const int p = q0 + f * THREADS + tid;
-          store(maxima + p, cm);
-          *best = max(*best, rank_key<T>(cm, sp.chunk0 + p + 1));
-        }
+    for (int f = 0; f < kFlight; ++f) {
+      const int q = q0 + f * THREADS + tid;
+      if (q >= sp.body) continue;
+      const float cm = st.template add_chunk<T>(w[f], scale, slack);
+      if (TOP) {
+        store(maxima + q, cm);
+        *best = max(*best, rank_key<T>(cm, sp.chunk0 + q + 1));
       }
+    }
+  };
+  constexpr int kStep = kFlight * THREADS;
+  for (int q0 = 0; q0 < sp.body; q0 += 2 * kStep) {
+    load(next, q0 + kStep);
+    use(now, q0);
     if (q0 == 0) labels.gather();
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f)
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
+    if (q0 + kStep >= sp.body) break;
+    load(now, q0 + 2 * kStep);
+    use(next, q0 + kStep);
   }
   if (sp.body == 0) labels.gather();
   *u = labels.finish();
@@ -653,29 +658,32 @@ __device__ __forceinline__ void write_part(uint32_t (&now)[kFlight][kWords], con
     const int64_t at = sp.lo + sp.head + (int64_t)q * kPer<T>;
     return q < sp.body && within(at, at + kPer<T>, sp.lo, sp.hi, err);
   };
-  uint32_t next[kFlight][kWords], out[kWords];
+  uint32_t next[kFlight][kWords];
   if (r.zero) {  // not read at all: it may hold anything
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) out[i] = 0;
+    for (int i = 0; i < kWords; ++i) next[0][i] = 0;
     for (int q = tid; q < sp.body; q += THREADS)
-      if (in_row(q)) store_chunk(gb + (int64_t)q * kPer<T>, out);
+      if (in_row(q)) store_chunk(gb + (int64_t)q * kPer<T>, next[0]);
     return;
   }
-  for (int q0 = 0; q0 < sp.body; q0 += kFlight * THREADS) {
-    load_ahead<T, THREADS>(next, z, sp, q0 + kFlight * THREADS, err);
+  auto put = [&](uint32_t(*w)[kWords], int q0) {
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
       const int q = q0 + f * THREADS + tid;
       if (!in_row(q)) continue;
 #pragma unroll
       for (int i = 0; i < kPer<T> / 2; ++i)
-        put_pair(out, i, smooth<ENTROPY, OWN>(r, pair_of(now[f], i, T())), T());
-      store_chunk(gb + (int64_t)q * kPer<T>, out);
+        put_pair(w[f], i, smooth<ENTROPY, OWN>(r, pair_of(w[f], i, T())), T());
+      store_chunk(gb + (int64_t)q * kPer<T>, w[f]);
     }
-#pragma unroll
-    for (int f = 0; f < kFlight; ++f)
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) now[f][i] = next[f][i];
+  };
+  constexpr int kStep = kFlight * THREADS;
+  for (int q0 = 0; q0 < sp.body; q0 += 2 * kStep) {
+    load_ahead<T, THREADS>(next, z, sp, q0 + kStep, err);
+    put(now, q0);
+    if (q0 + kStep >= sp.body) break;
+    load_ahead<T, THREADS>(now, z, sp, q0 + 2 * kStep, err);
+    put(next, q0 + kStep);
   }
 }
 
