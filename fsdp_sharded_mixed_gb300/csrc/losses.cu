@@ -452,9 +452,8 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
 // The sums of a block's part of a row: each thread keeps kFlight chunks in
 // flight ahead of those that it works on, two sets of buffers taking turns (one
 // copied to the other: 92 instead of 89 us for loss and gradient of 4095 x 32000
-// bf16; four single ones in turn, the same
-// registers, took 238 us instead of 180 for 4096 x 151936 bf16). TOP: the table,
-// and the thread's best chunk.
+// bf16; four single ones in turn, the same registers: 238 instead of 180 us for
+// 4096 x 151936 bf16). TOP: the table, and the thread's best chunk.
 constexpr int kFlight = 2;
 // labels: its read() asks for a row's labels once the first chunks are on their
 // way, gather() for the logits that they name after the first of them were used,

@@ -108,6 +108,14 @@ def test_logprobs_rows(R, V, dtype):
     _check_logprobs(R, V, dtype, T=1.7)
 
 
+def test_rows_in_clusters_more_than_the_gpu_holds():
+    """Rows whose table (alternatives) or whose rows in flight (loss and gradient)
+    take several blocks a row although rows are many."""
+    _check_logprobs(200, 262147, FP32, k=5)
+    _check_distill(400, 90001, 8, BF16, T=1.5)
+    _check_distill(160, 50021, 8, FP32, in_place=True)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("lead", [0, 1, 2, 3, 5, 8, 13])
 @pytest.mark.parametrize("pad", [0, 1, 7, 32])
