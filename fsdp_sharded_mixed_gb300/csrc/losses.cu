@@ -1062,8 +1062,8 @@ int threads_of(const VocabLaunch& in) {
 //  - Few rows: until every SM has a block (the gradient alone, whose blocks need
 //    not meet: 16), as long as every thread has a chunk.
 //  - Loss and gradient in one call: the rows in flight are read twice, so they
-//    are to stay in L2 (8192 x 151936 bf16: 1063 us with one block, 966 with
-//    two, 993 with four).
+//    are to stay in L2 (8192 x 151936 bf16: 1057 us with one block, 963 with
+//    two, 1016 with four; 4062 x 64000 bf16: 180 with one, 183 with two).
 //  - Top alternatives: the table of a block's part stays under a quarter of an
 //    SM's shared memory.
 template <typename T, bool LOSS, bool GRAD, bool TOP>
