@@ -365,7 +365,8 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
     __syncthreads();  // total_of's last answer has been read
     if (tid == 0) sh.count = sh.total = 0;
     __syncthreads();
-    // (NaN where the bound is 0 or a NaN's key: nothing compares below it)
+    // Most chunks are decided by their maximum alone. Where it is the bound's value,
+    // or either of them is a NaN (the bound may be 0 or a NaN's key), the key decides.
     const float at_least = key_value<T>(bound);
     for (int p0 = tid; look && p0 < ch.count(); p0 += 32 * THREADS) {
       uint32_t reach = 0;
@@ -375,7 +376,7 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
         if (p >= ch.count()) break;
         const float most = value_of(ch.maxima[p]);
         if (most < at_least) continue;
-        if (most == at_least || p >= ch.sp.body) {
+        if (!(most > at_least) || p >= ch.sp.body) {
           const uint64_t key = ch.key(p);
           if (key < bound || key == 0) continue;
         }
@@ -421,8 +422,8 @@ __device__ __forceinline__ void select_top(const T* z, const Chunks<T>& ch, int 
       bound_of<T>(k, k + k / 4 + 2, [&](uint64_t b) { return __syncthreads_count(mine >= b); });
   int n = list_from(bound, mine >= bound);
   if (n > sh.capacity) {
-    // Very many in a few threads' chunks: the exact k-th best chunk leaves the
-    // elements of k chunks at most.
+    // Very many in a few threads' chunks: the exact k-th best chunk leaves k chunks
+    // at most (keys are unique), whose elements the list holds.
     bound = bound_of<T>(k, k, [&](uint64_t b) {
       int reach = 0;
       for (int p = tid; p < ch.count(); p += THREADS) reach += ch.key(p) >= b;
