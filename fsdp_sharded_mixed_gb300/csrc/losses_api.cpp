@@ -59,6 +59,19 @@ class Buffers {
 const char* const kLogits = "logits";
 const char* const kGrad = "d_logits";
 
+// The rows of one matrix: (rows - 1) * stride + vocab elements, kMaxExtent at most
+// (2^46 bytes of fp32, past any device's memory), so that no product of them wraps.
+constexpr int64_t kMaxExtent = int64_t(1) << 44;
+zs_status check_stride(const char* fn, const char* name, int64_t stride,
+                       const zs::VocabLaunch& a) {
+  if (stride < a.vocab || stride > int64_t(1) << 40)
+    return zs::fail(ZS_ERR_RANGE, "%s: %s %lld outside vocab..2^40", fn, name, (long long)stride);
+  if (a.rows > 1 && stride > (kMaxExtent - a.vocab) / (a.rows - 1))
+    return zs::fail(ZS_ERR_RANGE, "%s: %lld rows %s %lld apart are more than 2^44 elements", fn,
+                    (long long)a.rows, name, (long long)stride);
+  return ZS_OK;
+}
+
 // Sizes, dtype, stride and temperature.
 zs_status check_rows(const char* fn, const zs::VocabLaunch& a) {
   if (a.dtype != ZS_BF16 && a.dtype != ZS_FP32)
@@ -68,12 +81,9 @@ zs_status check_rows(const char* fn, const zs::VocabLaunch& a) {
   if (a.vocab < 1 || a.vocab > ZS_MAX_VOCAB)
     return zs::fail(ZS_ERR_RANGE, "%s: vocab %lld outside 1..%d", fn, (long long)a.vocab,
                     ZS_MAX_VOCAB);
-  if (a.row_stride < a.vocab || a.row_stride > int64_t(1) << 40)
-    return zs::fail(ZS_ERR_RANGE, "%s: row_stride %lld outside vocab..2^40", fn,
-                    (long long)a.row_stride);
-  if (a.d_logits && (a.grad_stride < a.vocab || a.grad_stride > int64_t(1) << 40))
-    return zs::fail(ZS_ERR_RANGE, "%s: grad_stride %lld outside vocab..2^40", fn,
-                    (long long)a.grad_stride);
+  if (zs_status st = check_stride(fn, "row_stride", a.row_stride, a)) return st;
+  if (a.d_logits)
+    if (zs_status st = check_stride(fn, "grad_stride", a.grad_stride, a)) return st;
   if (!std::isfinite(a.temperature) || !(a.temperature > 0) ||
       !std::isfinite((float)(1.0 / a.temperature)) || !((float)(1.0 / a.temperature) > 0))
     return zs::fail(ZS_ERR_INVAL, "%s: temperature must be finite and > 0 (got %g)", fn,

@@ -468,7 +468,8 @@ zs_status zs_trace_first_divergence(const char* const* paths, int32_t n_paths, i
  *                     type's own alignment is needed, for these and for every
  *                     other buffer of these calls.
  *   vocab             1..ZS_MAX_VOCAB. rows 0..2^31-1; with rows == 0 the call
- *                     succeeds and touches nothing.
+ *                     succeeds and touches nothing. Strides up to 2^40, and
+ *                     (rows - 1) * stride + vocab up to 2^44.
  *   targets           int64 [rows] token ids; a negative id (ignore_index) is a
  *                     row without a token: its logprob is 0 and d_logprob is
  *                     taken as 0. An id >= vocab gives logprob NaN, counts as
