@@ -475,8 +475,8 @@ zs_status zs_trace_first_divergence(const char* const* paths, int32_t n_paths, i
  *                     taken as 0. An id >= vocab gives logprob NaN, counts as
  *                     no token in the gradient, and sets the device error word
  *                     (zs_check_device_error: ZS_ERR_RANGE).
- *   temperature       T, finite and > 0. With y = z / T: lse = ln sum_j exp(y_j),
- *                     ln p_j = y_j - lse.
+ *   temperature       T, 1e-38..1e37 (what fp32 holds both ways). With y = z / T:
+ *                     lse = ln sum_j exp(y_j), ln p_j = y_j - lse.
  *   Masked logits are -infinity (p = 0, and 0 ln 0 = 0) or any finite low value.
  *   A row masked throughout has lse = -infinity, logprob -infinity, entropy 0
  *   and an all-zero gradient. A NaN or +infinity makes the row's statistics NaN.

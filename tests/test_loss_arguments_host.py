@@ -1,5 +1,5 @@
 """Arguments of the vocabulary-row losses that no call has in earnest, refused
-before any CUDA call: extents past 64 bits."""
+before any CUDA call: extents past 64 bits, temperatures past fp32."""
 import numpy as np
 import pytest
 
@@ -43,3 +43,21 @@ def test_the_largest_extents_are_not():
         with pytest.raises(zs.ZsError) as e:
             _logprobs(zs.ZS_FP32, rows, stride=stride)
         assert e.value.status == zs.ZS_ERR_INVAL, str(e.value)
+
+
+@pytest.mark.parametrize("T", [1e-39, 3e-39, 4.2e-39, 9e-39, 2e37, 1e38, 1e40, 7e44])
+def test_temperatures_past_fp32_are_refused(T):
+    """Of these 1/T or log2(e)/T is infinite in fp32 or below its normal range, or
+    ln(vocab) T is infinite."""
+    for call in (_logprobs, _logprobs_grad):
+        with pytest.raises(zs.ZsError, match="temperature") as e:
+            call(T=T)
+        assert e.value.status == zs.ZS_ERR_INVAL
+
+
+@pytest.mark.parametrize("T", [1e-38, 1e-9, 1.0, 1e9, 1e37])
+def test_temperatures_within_fp32_are_not(T):
+    for call in (_logprobs, _logprobs_grad):
+        with pytest.raises(zs.ZsError) as e:
+            call(T=T)
+        assert "temperature" not in str(e.value)
