@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     float A = 0.0f, B = 0.0f, A1 = 0.0f, M1 = M, at_target = 0.0f;
     bool zero;
     if (LOSS) {
-      zero = lse == -INFINITY;
+      zero = empty;  // (lse may be -infinity without: the lowest value over T < 1)
       A = w * a.inv_t * Q / S;
       if (OWN)
         A1 = -al / S1;

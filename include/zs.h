@@ -480,6 +480,11 @@ zs_status zs_trace_first_divergence(const char* const* paths, int32_t n_paths, i
  *   Masked logits are -infinity (p = 0, and 0 ln 0 = 0) or any finite low value.
  *   A row masked throughout has lse = -infinity, logprob -infinity, entropy 0
  *   and an all-zero gradient. A NaN or +infinity makes the row's statistics NaN.
+ *   Of a row whose largest logit is itself a low value (the type's lowest, say)
+ *   lse no longer holds ln sum exp beside it, or is -infinity (past fp32's range,
+ *   at T < 1): every other output is as ever, the gradient calls that start from
+ *   lse get what p = exp(y - lse) gives (at lse = -infinity zero), and
+ *   zs_distill_loss_grad, which needs no lse, gets the row's gradient.
  *   Sums, maxima and statistics are fp32; a bf16 gradient is rounded once, to
  *   nearest even. Results do not depend on timing: the same call gives the same
  *   bits. d_logits (dtype of the logits, row r at r * grad_stride) may be the

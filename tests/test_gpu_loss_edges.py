@@ -1,0 +1,77 @@
+"""The losses over vocabulary rows where a value leaves the usual range."""
+import math
+
+import pytest
+import torch
+
+import fsdp_sharded_mixed_gb300 as zs
+import loss_reference as ref
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+CODE = {torch.bfloat16: zs.ZS_BF16, torch.float32: zs.ZS_FP32}
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def _f32(R):
+    return torch.full((R,), 777.0, dtype=FP32, device=DEV)
+
+
+# ---- scaled logits past fp32's range ---------------------------------------------
+def _lowest_rows(V, dtype):
+    """Rows whose largest logit is the type's lowest value: everywhere, in half of
+    the columns (the others masked), and in one; the ids of a teacher's record and
+    the target of each, among the columns that are left."""
+    z = torch.full((3, V), torch.finfo(dtype).min, dtype=dtype)
+    z[1, V // 2:] = -math.inf
+    z[2, 1:] = -math.inf
+    ids = torch.tensor([[V - 1, 0, 2], [1, V // 2 - 1, -1], [0, -1, -1]], dtype=torch.int32)
+    return z, ids, torch.tensor([2, 1, 0])
+
+
+def _lowest_gradients(z, ids, t, targets, w, h, T):
+    """(of the soft loss, of the hard labels): p is uniform over what is left."""
+    p = (~torch.isneginf(z)).double()
+    p = p / p.sum(1, keepdim=True)
+    q = torch.softmax(torch.where(ids >= 0, t.double() / T, -math.inf), 1)
+    soft = (w.double() / T)[:, None] * p
+    soft.scatter_add_(1, ids.clamp(min=0).long(), -(w.double() / T)[:, None] * q)
+    hard = -h.double()[:, None] * p
+    hard.scatter_add_(1, targets[:, None], h.double()[:, None])
+    return soft, hard
+
+
+def _within(got, want, rel, scale, bf16):
+    """rel of what the terms add up from, and a bf16 result's own rounding."""
+    tol = rel * scale + (want.abs() * ref.BF16_ROUNDING if bf16 else 0.0)
+    got = got.detach().cpu().double()
+    assert bool(((got - want).abs() <= tol).all()), (got - want).abs().max()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [5, 1000, 50257])
+@pytest.mark.parametrize("T", [0.3, 0.7])
+def test_rows_of_the_lowest_value_sharpened(T, V, dtype):
+    """The lowest value over T < 1 is past fp32's range, so is the row's lse; its
+    probabilities, losses and gradients are not."""
+    z, ids, targets = _lowest_rows(V, dtype)
+    t = torch.tensor([[1.0, 0.5, -1.0], [2.0, 0.0, 9.0], [0.0, 9.0, 9.0]])
+    w, h = torch.tensor([0.5, 2.0, 1.0]), torch.tensor([-0.25, 1.0, -3.0])
+    R, out = 3, [_f32(3) for _ in range(4)]
+    grad = torch.empty(R, V, dtype=dtype, device=DEV)
+    head = (z.to(DEV), CODE[dtype], R, V, V, ids.to(DEV), t.to(DEV), zs.ZS_FP32, 3, None, T,
+            targets.to(DEV))
+    zs.zs_distill_loss_grad(*head, w.to(DEV), h.to(DEV), *out, grad, V)
+    soft, hard = _lowest_gradients(z, ids, t, targets, w, h, T)
+    # sums and quotients of equal terms: tol_sum's roundings and some 16 more
+    rel = ref.tol_sum(V) + 32 * ref.EPS
+    scale = (w / T + h.abs()).double()[:, None] * 2
+    _within(grad, soft + hard, rel, scale, dtype == BF16)
+    loss, lse, logprob, hard_lse = out
+    assert bool(torch.isneginf(lse).all()) and bool(torch.isfinite(hard_lse).all())
+    live = (~torch.isneginf(z)).sum(1).double()
+    _within(logprob, -live.log(), rel, 2 * live.log()[:, None].amax() + 1, False)
+    q = torch.softmax(torch.where(ids >= 0, t.double() / T, -math.inf), 1)
+    want = torch.where(q > 0, q * (torch.where(q > 0, q, 1.0).log() + live.log()[:, None]), 0.0)
+    _within(loss, want.sum(1), rel, 2 * live.log().amax() + 8, False)
