@@ -908,7 +908,9 @@ __global__ void __launch_bounds__(THREADS, kResident / THREADS)
     const float u0 = a.teacher_lse ? labels.teacher_lse : u_max == -INFINITY ? 0.0f : u_max;
     float x_sum = 0.0f, l_sum = 0.0f;
     for (int k = tid; k < K; k += THREADS) {
-      const float ln_x = sl.q[k] - u0, x = expf(ln_x);
+      // (an entry without mass has none whatever u0: a teacher's row masked
+      // throughout has lse -infinity)
+      const float ln_x = sl.q[k] - u0, x = sl.q[k] == -INFINITY ? 0.0f : expf(ln_x);
       sl.q[k] = x;
       x_sum += x;
       if (LOSS && !(x == 0.0f))

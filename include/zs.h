@@ -533,9 +533,9 @@ zs_status zs_token_logprobs_grad(const void* logits, zs_dtype dtype, int64_t row
  *                     zeros as teacher_lse.)
  *   targets           NULL, or hard labels: logprob [rows] = ln p of the target
  *                     at T = 1, and hard_lse [rows] = lse at T = 1.
- * loss and lse (at T) fp32 [rows]. Each output may be NULL, not all. A row
- * without teacher entries has loss 0; an entry with q_k > 0 on a masked logit
- * makes the loss +infinity. */
+ * loss and lse (at T) fp32 [rows]. Each output may be NULL, not all. An entry of
+ * -infinity has q_k = 0, and a row without other entries loss 0, whatever its
+ * teacher_lse; an entry with q_k > 0 on a masked logit makes the loss +infinity. */
 zs_status zs_distill_loss(const void* logits, zs_dtype dtype, int64_t rows, int64_t vocab,
                           int64_t row_stride, const int32_t* teacher_ids,
                           const void* teacher_logits, zs_dtype teacher_dtype, int32_t teacher_k,

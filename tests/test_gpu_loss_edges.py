@@ -1,4 +1,5 @@
-"""The losses over vocabulary rows where a value leaves the usual range."""
+"""The losses over vocabulary rows where a value leaves the usual range, and
+teachers without mass."""
 import math
 
 import pytest
@@ -75,3 +76,37 @@ def test_rows_of_the_lowest_value_sharpened(T, V, dtype):
     q = torch.softmax(torch.where(ids >= 0, t.double() / T, -math.inf), 1)
     want = torch.where(q > 0, q * (torch.where(q > 0, q, 1.0).log() + live.log()[:, None]), 0.0)
     _within(loss, want.sum(1), rel, 2 * live.log().amax() + 8, False)
+
+
+# ---- teachers without mass -------------------------------------------------------
+@pytest.mark.parametrize("K", [1, 5, 200])
+def test_teacher_rows_masked_throughout_have_no_loss(K):
+    """A teacher's row masked throughout has lse = -infinity: its record, unused
+    entries or entries of -infinity, adds nothing to the loss or the gradient."""
+    R, V = 4, 3001
+    g = torch.Generator().manual_seed(K)
+    z = torch.randn(R, V, generator=g)
+    ids = torch.randint(0, V, (R, K), generator=g, dtype=torch.int32)
+    t = torch.randn(R, K, generator=g)
+    ids[0] = -1
+    t[1] = -math.inf
+    ids[2] = -1
+    lse = torch.tensor([-math.inf, -math.inf, math.nan, 9.0])   # (row 2: of a row not recorded)
+    targets = torch.randint(0, V, (R,), generator=g)
+    one = torch.ones(R, device=DEV)
+    d = lambda x: x.to(DEV)  # noqa: E731
+    head = (d(z), zs.ZS_FP32, R, V, V, d(ids), d(t), zs.ZS_FP32, K, d(lse), 1.0, d(targets))
+    own, grad = _f32(R), torch.empty(R, V, device=DEV)
+    loss, lse_s, hard_lse = _f32(R), _f32(R), _f32(R)
+    zs.zs_distill_loss(*head, own, lse_s, None, hard_lse)
+    zs.zs_distill_loss_grad(*head, one, one, loss, None, None, None, grad, V)
+    alone = torch.empty_like(grad)
+    zs.zs_distill_grad(*head, lse_s, hard_lse, one, one, alone, V)
+    assert loss[:3].tolist() == own[:3].tolist() == [0.0, 0.0, 0.0]
+    assert bool(torch.isfinite(loss[3])) and torch.equal(loss, own)
+    p = torch.softmax(z.double(), 1)
+    want = -p
+    want.scatter_add_(1, targets[:, None], torch.ones(R, 1, dtype=torch.float64))
+    rel = ref.tol_sum(V) + 64 * ref.EPS    # of p <= 1, and of the normalisers' size (about 8)
+    for got in (grad, alone):
+        _within(got[:3], want[:3], rel, 1.0, False)
