@@ -746,9 +746,10 @@ extern "C" zs_status zs_check_device_error(void* cuda_stream) {
   if (e != cudaSuccess)
     return zs::fail(ZS_ERR_CUDA, "zs_check_device_error: %s", cudaGetErrorString(e));
   if (word & 2u) return zs::fail(ZS_ERR_TIMEOUT, "zs_check_device_error: a device wait timed out");
-  if (word & 1u)
-    return zs::fail(ZS_ERR_RANGE, "zs_check_device_error: a bounds check failed, or a token id "
-                                  "was out of range");
+  if (word & 1u) return zs::fail(ZS_ERR_RANGE, "zs_check_device_error: a bounds check failed");
+  if (word & 4u)
+    return zs::fail(ZS_ERR_RANGE,
+                    "zs_check_device_error: a token id given to a loss is outside the vocabulary");
   return ZS_OK;
 }
 

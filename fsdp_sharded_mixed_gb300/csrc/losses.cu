@@ -747,7 +747,7 @@ struct Labels {
   }
   __device__ __forceinline__ int32_t checked(int32_t id) const {
     if (id < a.vocab) return id;
-    if (first) atomicOr(a.err, 1u);
+    if (first) atomicOr(a.err, 4u);
     return -1;
   }
   __device__ __forceinline__ void put(int k, int32_t id, uint32_t t, float zk, float* u) {
@@ -779,7 +779,7 @@ struct Labels {
     my_id = checked(my_id);
     if (wanted(my_id)) my_z = z[my_id];
     bad_target = raw_target >= a.vocab;
-    if (bad_target && first && threadIdx.x == 0) atomicOr(a.err, 1u);
+    if (bad_target && first && threadIdx.x == 0) atomicOr(a.err, 4u);
     if (raw_target >= 0 && !bad_target) target = (int32_t)raw_target;
     if (wanted(target)) z_target = z[target];
     if (target < 0) al = 0.0f;

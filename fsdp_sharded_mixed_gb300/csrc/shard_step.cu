@@ -35,8 +35,9 @@
 
 namespace zs {
 
-// Bit value 1: a check of the bounds-checked build failed, or a token id given to
-// a loss was outside the vocabulary; 2: a bounded wait gave up. Read and cleared by zs_check_device_error.
+// Bit value 1: a check of the bounds-checked build failed; 2: a bounded wait
+// gave up; 4: a token id given to a loss was outside the vocabulary. Read and
+// cleared by zs_check_device_error.
 __device__ unsigned int g_error_word;
 
 int bounds_checked() { return ZS_BOUNDS_CHECK; }

@@ -210,8 +210,8 @@ unsigned int* device_error_word();
 // One block waiting, bounded by `polls`, on an mbarrier nothing arrives on.
 cudaError_t launch_wait_timeout(uint32_t polls, cudaStream_t stream);
 
-// Device error word: bit value 1 set by the bounds-checked build's checks and by
-// token ids outside the vocabulary, 2 by bounded waits that gave up.
+// Device error word: bit value 1 set by the bounds-checked build's checks, 2 by
+// bounded waits that gave up, 4 by token ids outside the vocabulary.
 cudaError_t read_and_clear_device_error(cudaStream_t stream, unsigned int* word);
 
 int elem_bytes(zs_dtype dt);

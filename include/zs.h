@@ -576,8 +576,8 @@ const char* zs_last_error(void);
 /* Synchronises `cuda_stream`, then reads and clears this device's error word
  * (set by the bounds-checked build's checks, by bounded waits, and by token ids
  * outside the vocabulary);
- * ZS_ERR_TIMEOUT or ZS_ERR_RANGE if it was set, ZS_ERR_CUDA if the stream
- * reports an error. The library looks the addresses of its device arrays
+ * ZS_ERR_TIMEOUT (a wait) or ZS_ERR_RANGE (a check, else a token id: the message
+ * says which) if it was set, ZS_ERR_CUDA if the stream reports an error. The library looks the addresses of its device arrays
  * (this error word, the no-alloc norm scratch) up once per device and keeps
  * them for the life of the process: it is not to be used across a
  * cudaDeviceReset of a device it has used. */

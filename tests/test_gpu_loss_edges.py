@@ -1,5 +1,6 @@
-"""The losses over vocabulary rows where a value leaves the usual range, and
-teachers without mass."""
+"""The losses over vocabulary rows where a value leaves the usual range,
+teachers without mass, and ids out of range beside the checks of the
+bounds-checked build."""
 import math
 
 import pytest
@@ -110,3 +111,22 @@ def test_teacher_rows_masked_throughout_have_no_loss(K):
     rel = ref.tol_sum(V) + 64 * ref.EPS    # of p <= 1, and of the normalisers' size (about 8)
     for got in (grad, alone):
         _within(got[:3], want[:3], rel, 1.0, False)
+
+
+# ---- ids out of range --------------------------------------------------------------
+def test_ids_out_of_range_are_told_from_failed_bounds_checks():
+    R, V = 2, 100
+    z = torch.zeros(R, V, device=DEV)
+    zs.zs_check_device_error()
+    zs.zs_token_logprobs(z, zs.ZS_FP32, R, V, V, torch.tensor([1, V], device=DEV), 1.0, _f32(R))
+    with pytest.raises(zs.ZsError, match="token id") as e:
+        zs.zs_check_device_error()
+    assert e.value.status == zs.ZS_ERR_RANGE
+    assert "bounds check" not in str(e.value)
+    ids = torch.tensor([[0, 1], [2, V]], dtype=torch.int32, device=DEV)
+    zs.zs_distill_loss(z, zs.ZS_FP32, R, V, V, ids, torch.zeros(R, 2, device=DEV), zs.ZS_FP32, 2,
+                       None, 1.0, None, _f32(R))
+    with pytest.raises(zs.ZsError, match="token id") as e:
+        zs.zs_check_device_error()
+    assert "bounds check" not in str(e.value)
+    zs.zs_check_device_error()   # read and cleared
