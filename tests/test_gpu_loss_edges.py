@@ -1,6 +1,6 @@
-"""The losses over vocabulary rows where a value leaves the usual range,
-teachers without mass, and ids out of range beside the checks of the
-bounds-checked build."""
+"""The losses over vocabulary rows where a value leaves the usual range: scaled
+logits past fp32's, teachers without mass, ids out of range beside the checks of
+the bounds-checked build, and tokens the model is all but sure of."""
 import math
 
 import pytest
@@ -130,3 +130,37 @@ def test_ids_out_of_range_are_told_from_failed_bounds_checks():
         zs.zs_check_device_error()
     assert "bounds check" not in str(e.value)
     zs.zs_check_device_error()   # read and cleared
+
+
+# ---- tokens the model is all but sure of -------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T", [1.0, 2.0])
+@pytest.mark.parametrize("R", [3, 200])
+def test_likely_tokens_keep_their_small_values(R, T, dtype):
+    """Two logits left of a row, the likely one behind the other in the same
+    thread's share (every block size divides 256 chunks) and 4.5 to 5.5 T above.
+
+    Bounds: with the sums relative to the maximum, S = 1 + x, x = e^-d: one rounding
+    of S (EPS), x itself to (3 d / ln 2 + 4) EPS, ln S to EPS of its size; U = -x d /
+    ln 2 has x's error and two roundings, the entropy one more of its own size."""
+    V, chunk = 32000, 32 // torch.finfo(dtype).bits * 8
+    low, high = 16 * chunk, (16 + 256) * chunk
+    z = torch.full((R, V), -math.inf)
+    z[:, low] = torch.arange(R) / R
+    z[:, high] = z[:, low] + T * (4.5 + torch.rand(R, generator=torch.Generator().manual_seed(4)))
+    z = z.to(dtype)
+    logprob, H, lse = _f32(R), _f32(R), _f32(R)
+    top = torch.empty(R, 2, device=DEV)
+    ids = torch.empty(R, 2, dtype=torch.int32, device=DEV)
+    target = torch.full((R,), high, dtype=torch.int64, device=DEV)
+    zs.zs_token_logprobs(z.to(DEV), CODE[dtype], R, V, V, target, T, logprob, H, lse, 2, ids, top)
+    d = ((z[:, high].double() - z[:, low].double()) / T)
+    x = torch.exp(-d)
+    ln_s = torch.log1p(x)
+    each = (3 * d / math.log(2) + 4) * ref.EPS
+    tol = ref.EPS * (1 + 2 * ln_s) + x * each
+    assert bool(((logprob.cpu().double() + ln_s).abs() <= tol).all())
+    assert bool(((top[:, 0].cpu().double() + ln_s).abs() <= tol).all())
+    want = ln_s + x * d / (1 + x)
+    tol = tol + x * d * (each + 4 * ref.EPS) + ref.EPS * want
+    assert bool(((H.cpu().double() - want).abs() <= tol).all())
