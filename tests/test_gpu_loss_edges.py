@@ -1,6 +1,7 @@
 """The losses over vocabulary rows where a value leaves the usual range: scaled
 logits past fp32's, teachers without mass, ids out of range beside the checks of
-the bounds-checked build, and tokens the model is all but sure of."""
+the bounds-checked build, tokens the model is all but sure of, and losses without
+a teacher."""
 import math
 
 import pytest
@@ -9,6 +10,7 @@ import torch
 import fsdp_sharded_mixed_gb300 as zs
 import loss_reference as ref
 from gpu_util import DEV
+from test_gpu_losses import _check_distill
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +166,13 @@ def test_likely_tokens_keep_their_small_values(R, T, dtype):
     want = ln_s + x * d / (1 + x)
     tol = tol + x * d * (each + 4 * ref.EPS) + ref.EPS * want
     assert bool(((H.cpu().double() - want).abs() <= tol).all())
+
+
+# ---- no teacher --------------------------------------------------------------------
+@pytest.mark.parametrize("mode", ["loss", "grad", "fused"])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("R,V", [(1, 1), (5, 33), (700, 1000), (153, 4099), (3, 50257),
+                                 (2, 151936), (200, 90001)])
+def test_cross_entropy_without_a_teacher(R, V, dtype, mode):
+    _check_distill(R, V, 0, dtype, mode=mode)
+    _check_distill(R, V, 0, dtype, T=1.5, mode=mode, in_place=mode != "loss", mask="lowest")
