@@ -18,12 +18,14 @@
 // Bound: HBM. A call reads its logits once (V * 2 or 4 bytes a row) and, with
 // a gradient, writes as much; 6 to 15 flops and one or two exponentials an
 // element. On GB300, as a share of the measured copy bandwidth (6779 GB/s):
-// scoring 4096 x 151936 bf16 178 us = 1.03; evaluating 8192 x 32000 bf16, T = 2
-// with hard labels, 85.4 us = 0.91; the gradient alone of 8192 x 50257 bf16 237 us
-// = 0.99; loss and gradient in one call 0.87 (4095 x 32000, 89.0 us) and 0.76
-// (8192 x 151936, 963 us), where a block's reading and writing take turns; 64
-// alternatives of 8191 x 32000 fp32 218 us = 0.71, the search coming after the
-// stream. Small calls take 3 to 8 us of GPU time, less than a call from Python.
+// scoring 4096 x 151936 bf16 180 us = 1.02; evaluating 8192 x 32000 bf16, T = 2
+// with hard labels, 85.3 us = 0.91; the gradient alone of 8192 x 50257 bf16 237 us
+// = 0.99; loss and gradient in one call 0.87 (4095 x 32000, 89.3 us) and 0.77
+// (8192 x 151936, 954 us), where a block's reading and writing take turns; 64
+// alternatives of 8191 x 32000 fp32 220 us = 0.71, the search coming after the
+// stream. Short rows are bound by what a row takes beside its bytes (16384 x 1000
+// bf16: 17.4 us = 0.28, with 20 alternatives 62 us = 0.09). Small calls take 3 to
+// 8 us of GPU time, less than a call from Python.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -672,7 +674,7 @@ __device__ __forceinline__ void write_part(uint32_t (&now)[kFlight][kWords], con
     return q < sp.body && within(at, at + kPer<T>, sp.lo, sp.hi, err);
   };
   uint32_t next[kFlight][kWords];
-  if (r.zero) {  // not read at all: it may hold anything
+  if (r.zero) {  // what load_ahead brought is not used: the row may hold anything
 #pragma unroll
     for (int i = 0; i < kWords; ++i) next[0][i] = 0;
     for (int q = tid; q < sp.body; q += THREADS)
@@ -1077,8 +1079,13 @@ int threads_of(const VocabLaunch& in) {
 //  - Few rows: until every SM has a block (the gradient alone, whose blocks need
 //    not meet: 16), as long as every thread has a chunk.
 //  - Loss and gradient in one call: the rows in flight are read twice, so they
-//    are to stay in L2 (8192 x 151936 bf16: 1057 us with one block, 963 with
-//    two, 1016 with four; 4062 x 64000 bf16: 180 with one, 183 with two).
+//    are to stay in L2. With one, two and four blocks, us, the rule's in brackets:
+//      bf16  4062 x 64000 [180.5] 182.5 -, 2031 x 128000 218 [184.8] 188.6,
+//            1711 x 151936 225 [195.5] 188.6, 8192 x 151936 1065 [954] 983
+//      fp32  4062 x 64000 431 [361.8] 361, 2031 x 128000 430 [363.4] 373,
+//            1711 x 151936 440 [387] 379.5
+//    (a few rounds of the largest rows want four, many want two: by bytes alone the
+//    rule is up to 4 % from the better one there).
 //  - Top alternatives: the table of a block's part stays under a quarter of an
 //    SM's shared memory.
 template <typename T, bool LOSS, bool GRAD, bool TOP>
