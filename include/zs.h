@@ -489,7 +489,9 @@ zs_status zs_trace_first_divergence(const char* const* paths, int32_t n_paths, i
  *   nearest even. Results do not depend on timing: the same call gives the same
  *   bits. d_logits (dtype of the logits, row r at r * grad_stride) may be the
  *   logits themselves with the same stride; any other overlap of an output is
- *   ZS_ERR_INVAL. Elements between vocab and the strides are not touched.
+ *   ZS_ERR_INVAL (a matrix counts from its first element to its last, so one kept
+ *   between another's rows overlaps it). Elements between vocab and the strides
+ *   are not touched.
  * Errors: ZS_ERR_INVAL (NULL, dtype, temperature, overlap, not device memory),
  * ZS_ERR_RANGE (sizes), ZS_ERR_ALIGN, ZS_ERR_CUDA.
  *
