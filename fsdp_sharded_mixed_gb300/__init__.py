@@ -13,7 +13,8 @@ FSDP2 row layout (``zs_rows_plan``, ``zs_unshard``, ``zs_shard_rows``);
 clipping, accumulation, and the sharded checkpoint (``zs_checkpoint_save``,
 ``zs_checkpoint_load``: host file I/O of host- or device-resident state); the
 losses over vocabulary rows that make the gradients (``zs_token_logprobs``,
-``zs_distill_loss`` and their gradients).
+``zs_distill_loss`` and their gradients); the operators around the layers
+(``zs_embedding``, ``zs_layer_norm`` and their gradients, ``zs_tensors_clip``).
 """
 from __future__ import annotations
 
@@ -40,14 +41,16 @@ ZS_BF16, ZS_FP32, ZS_FP24 = 0, 1, 2
 ELEM_BYTES = {ZS_BF16: 2, ZS_FP32: 4, ZS_FP24: 3}
 ZS_MAX_WORLD = 1024
 ZS_MAX_VOCAB, ZS_MAX_TOP, ZS_MAX_TEACHER = 1 << 20, 128, 256
+ZS_MAX_DIM, ZS_MAX_TENSORS = 32768, 65536
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", *ARCH, "-lineinfo", "-fmad=false", "-prec-div=true",
               "-prec-sqrt=true", "-ftz=false", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-pthread", "-I/usr/local/cuda/include"]
 CUDA_SOURCES = ["shard_step.cu", "gather.cu", "clip.cu", "accum.cu", "rows.cu", "ckpt.cu",
-                "losses.cu"]
-HOST_SOURCES = ["api.cpp", "plan.cpp", "checkpoint.cpp", "trace.cpp", "losses_api.cpp"]
+                "losses.cu", "embedding.cu", "layer_norm.cu", "tensors.cu"]
+HOST_SOURCES = ["api.cpp", "plan.cpp", "checkpoint.cpp", "trace.cpp", "losses_api.cpp",
+                "layers_api.cpp"]
 
 
 # ----------------------------------------------------------------- build ----
@@ -165,6 +168,21 @@ EXPORTS = {
     "zs_distill_loss_grad": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_int, _I32, _P,
                               ctypes.c_double, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P],
                              ctypes.c_int),
+    "zs_embedding": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64, ctypes.c_double, _P,
+                      ctypes.c_int, _I64, _P], ctypes.c_int),
+    "zs_embedding_grad_workspace_bytes": ([_I64, _I64], _I64),
+    "zs_embedding_grad": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64, ctypes.c_double, _P, _P,
+                           _I64, _P, ctypes.c_int, _I64, _P], ctypes.c_int),
+    "zs_layer_norm": ([_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P, ctypes.c_int,
+                       ctypes.c_double, _P, _P, _I64, _P, _P, _P], ctypes.c_int),
+    "zs_layer_norm_grad_workspace_bytes": ([_I64, _I64], _I64),
+    "zs_layer_norm_grad": ([_P, _P, ctypes.c_int, _I64, _I64, _I64, _I64, _P, ctypes.c_int, _P,
+                            _P, _P, _P, _I64, _P, _P, _P, ctypes.c_int, _P], ctypes.c_int),
+    "zs_tensors_sqnorm": ([_P, _P, _I32, ctypes.c_int, _P, _I64, _P, _P], ctypes.c_int),
+    "zs_tensors_scale": ([_P, _P, _I32, ctypes.c_int, _P, _P, _P, ctypes.c_int, _P],
+                         ctypes.c_int),
+    "zs_tensors_clip": ([_P, _P, _I32, ctypes.c_int, ctypes.c_double, _P, ctypes.c_int, _P, _I64,
+                         _P, _P, _P, _P], ctypes.c_int),
     "zs_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "zs_last_error": ([], ctypes.c_char_p),
     "zs_check_device_error": ([_P], ctypes.c_int),
@@ -657,6 +675,152 @@ def zs_distill_loss_grad(logits, dtype, rows, vocab, row_stride, teacher_ids, te
         _row_ptr(logprob, n, fn, "logprob"), _row_ptr(hard_lse, n, fn, "hard_lse"),
         _rows_ptr(d_logits, rows, vocab, grad_stride, dtype, fn, "d_logits"), grad_stride,
         _stream(stream)))
+
+
+def zs_embedding(table, table_dtype, vocab, dim, table_stride, tokens, rows, scale, out,
+                 out_dtype, out_stride, stream=None):
+    """Enqueue ``out[r] = scale * table[tokens[r]]`` (``tokens`` int64; a negative
+    id gives a row of zeros) for a ``vocab`` x ``dim`` table; rows start
+    ``table_stride`` and ``out_stride`` elements apart."""
+    fn = "zs_embedding"
+    _check(lib().zs_embedding(
+        _rows_ptr(table, vocab, dim, table_stride, table_dtype, fn, "table"), table_dtype, vocab,
+        dim, table_stride, _row_ptr(tokens, 8 * rows, fn, "tokens"), rows, scale,
+        _rows_ptr(out, rows, dim, out_stride, out_dtype, fn, "out"), out_dtype, out_stride,
+        _stream(stream)))
+
+
+def zs_embedding_grad_workspace_bytes(rows, dim):
+    return lib().zs_embedding_grad_workspace_bytes(rows, dim)
+
+
+def zs_embedding_grad(d_out, dtype, rows, dim, row_stride, tokens, vocab, scale, add_to,
+                      workspace, d_table, table_dtype, table_stride, stream=None):
+    """Enqueue the table's gradient, ``d_table[v] = add_to[v] + scale * sum of
+    d_out[r] over tokens[r] == v``; ``add_to`` None = zero, or ``d_table`` itself
+    to add in place; ``workspace``: device scratch of
+    ``zs_embedding_grad_workspace_bytes(rows, dim)``."""
+    fn = "zs_embedding_grad"
+    _check(lib().zs_embedding_grad(
+        _rows_ptr(d_out, rows, dim, row_stride, dtype, fn, "d_out"), dtype, rows, dim, row_stride,
+        _row_ptr(tokens, 8 * rows, fn, "tokens"), vocab, scale,
+        _rows_ptr(add_to, vocab, dim, table_stride, table_dtype, fn, "add_to"), _ptr(workspace),
+        _scratch_bytes(workspace, lib().zs_embedding_grad_workspace_bytes, rows, dim),
+        _rows_ptr(d_table, vocab, dim, table_stride, table_dtype, fn, "d_table"), table_dtype,
+        table_stride, _stream(stream)))
+
+
+def _scratch_bytes(workspace, needed, *sizes):
+    """A workspace's bytes; of an address those that the call needs (the caller's
+    responsibility)."""
+    if workspace is None:
+        return 0
+    return needed(*sizes) if isinstance(workspace, int) else workspace.nbytes
+
+
+def zs_layer_norm(x, dtype, rows, dim, row_stride, residual, weight, bias, weight_dtype, eps,
+                  sum_out, y, out_stride, mean=None, rstd=None, stream=None):
+    """Enqueue layer norm of each row of ``x`` (+ ``residual``, the sum rounded
+    and left in ``sum_out``) into ``y``; ``weight``, ``bias`` [dim] or None;
+    ``mean``, ``rstd``: fp32 [rows] for the backward pass, or None."""
+    fn, n, w = "zs_layer_norm", 4 * rows, ELEM_BYTES.get(weight_dtype, 0) * dim
+    _check(lib().zs_layer_norm(
+        _rows_ptr(x, rows, dim, row_stride, dtype, fn, "x"), dtype, rows, dim, row_stride,
+        _rows_ptr(residual, rows, dim, row_stride, dtype, fn, "residual"),
+        _row_ptr(weight, w, fn, "weight"), _row_ptr(bias, w, fn, "bias"), weight_dtype, eps,
+        _rows_ptr(sum_out, rows, dim, out_stride, dtype, fn, "sum_out"),
+        _rows_ptr(y, rows, dim, out_stride, dtype, fn, "y"), out_stride,
+        _row_ptr(mean, n, fn, "mean"), _row_ptr(rstd, n, fn, "rstd"), _stream(stream)))
+
+
+def zs_layer_norm_grad_workspace_bytes(rows, dim):
+    return lib().zs_layer_norm_grad_workspace_bytes(rows, dim)
+
+
+def zs_layer_norm_grad(d_y, x, dtype, rows, dim, grad_stride, row_stride, weight, weight_dtype,
+                       mean, rstd, d_sum, workspace, d_x, d_weight, d_bias, grad_dtype,
+                       stream=None):
+    """Enqueue layer norm's backward pass: ``d_x`` (with ``d_sum``, the gradient
+    past the norm, added; None = none), ``d_weight`` and ``d_bias`` ([dim] of
+    ``grad_dtype``, or None). ``x``: what was normalised; ``workspace``: device
+    scratch of ``zs_layer_norm_grad_workspace_bytes(rows, dim)``."""
+    fn, n = "zs_layer_norm_grad", 4 * rows
+    g = ELEM_BYTES.get(grad_dtype, 0) * dim
+    _check(lib().zs_layer_norm_grad(
+        _rows_ptr(d_y, rows, dim, grad_stride, dtype, fn, "d_y"),
+        _rows_ptr(x, rows, dim, row_stride, dtype, fn, "x"), dtype, rows, dim, grad_stride,
+        row_stride, _row_ptr(weight, ELEM_BYTES.get(weight_dtype, 0) * dim, fn, "weight"),
+        weight_dtype, _row_ptr(mean, n, fn, "mean"), _row_ptr(rstd, n, fn, "rstd"),
+        _rows_ptr(d_sum, rows, dim, grad_stride, dtype, fn, "d_sum"), _ptr(workspace),
+        _scratch_bytes(workspace, lib().zs_layer_norm_grad_workspace_bytes, rows, dim),
+        _rows_ptr(d_x, rows, dim, grad_stride, dtype, fn, "d_x"),
+        _row_ptr(d_weight, g, fn, "d_weight"), _row_ptr(d_bias, g, fn, "d_bias"), grad_dtype,
+        _stream(stream)))
+
+
+class Tensors(Buffers):
+    """A list of tensors of any lengths marshalled once (a model's gradients, or
+    their places in a flat buffer): addresses and lengths in ready C arrays. It
+    does not keep the tensors. Pass it, or the list itself, to ``zs_tensors_*``."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        super().__init__(tensors)
+        self.numels = (ctypes.c_int64 * max(len(tensors), 1))(*[t.numel() for t in tensors])
+        sizes = {t.element_size() for t in tensors}
+        if len(sizes) > 1:
+            raise ValueError("zs: the tensors of a list must have one dtype")
+        self.element_size = sizes.pop() if sizes else None
+
+
+def _tensors(x, dtype, fn, name):
+    x = x if isinstance(x, Tensors) else Tensors(x)
+    if x.element_size is not None and x.element_size != ELEM_BYTES.get(dtype, 0):
+        raise ValueError(f"{fn}: {name} has elements of {x.element_size} bytes, not dtype {dtype}'s")
+    return x
+
+
+def _outs(outs, out_dtype, tensors, fn):
+    o = _tensors(outs, out_dtype, fn, "outs")
+    if len(o) != len(tensors) or bytes(o.numels) != bytes(tensors.numels):
+        raise ValueError(f"{fn}: outs must have the lengths of the tensors")
+    return o
+
+
+def zs_tensors_sqnorm(tensors, dtype, workspace, sqnorm_out, stream=None):
+    """Enqueue the sum of squares over a list of ``tensors`` (or ``Tensors``) into
+    the device double ``sqnorm_out``; ``workspace``: device scratch of
+    ``zs_grad_norm_workspace_bytes()``."""
+    t = _tensors(tensors, dtype, "zs_tensors_sqnorm", "tensors")
+    _check(lib().zs_tensors_sqnorm(
+        t.array, t.numels, len(t), dtype, _ptr(workspace),
+        _scratch_bytes(workspace, lib().zs_grad_norm_workspace_bytes), _ptr(sqnorm_out),
+        _stream(stream)))
+
+
+def zs_tensors_scale(tensors, dtype, coef, skip, outs, out_dtype, stream=None):
+    """Enqueue ``outs[i] = tensors[i] * coef`` for a device fp32 ``coef``, unless
+    the device int32 ``skip`` (or None) is set; ``outs`` may be ``tensors``."""
+    fn = "zs_tensors_scale"
+    t = _tensors(tensors, dtype, fn, "tensors")
+    o = _outs(outs, out_dtype, t, fn)
+    _check(lib().zs_tensors_scale(t.array, t.numels, len(t), dtype, _ptr(coef), _ptr(skip),
+                                  o.array, out_dtype, _stream(stream)))
+
+
+def zs_tensors_clip(tensors, dtype, max_norm, outs, out_dtype, workspace, norm_out, coef_out,
+                    nonfinite_out, stream=None):
+    """Enqueue the global norm of a list of gradients, the coefficient ``min(1,
+    max_norm / (norm + 1e-6))`` and ``outs[i] = tensors[i] * coefficient`` (nothing
+    if the norm is not finite); ``outs`` may be ``tensors``. ``norm_out``,
+    ``coef_out``: device fp32, ``nonfinite_out``: device int32."""
+    fn = "zs_tensors_clip"
+    t = _tensors(tensors, dtype, fn, "tensors")
+    o = _outs(outs, out_dtype, t, fn)
+    _check(lib().zs_tensors_clip(
+        t.array, t.numels, len(t), dtype, max_norm, o.array, out_dtype, _ptr(workspace),
+        _scratch_bytes(workspace, lib().zs_grad_norm_workspace_bytes), _ptr(norm_out),
+        _ptr(coef_out), _ptr(nonfinite_out), _stream(stream)))
 
 
 def _io_stream(stream):

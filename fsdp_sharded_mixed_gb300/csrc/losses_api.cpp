@@ -3,72 +3,13 @@
 // anything is enqueued.
 #include <cuda_runtime.h>
 
+#include "buffers.h"
 #include "zs_internal.h"
 
 namespace {
 
-// The buffers of one call, checked as they are added: natural alignment here,
-// then (check) outputs against every other buffer and each one's residency.
-class Buffers {
- public:
-  explicit Buffers(const char* fn) : fn_(fn) {}
-
-  zs_status add(const char* name, const void* p, int64_t bytes, int align, bool output) {
-    if ((uintptr_t)p % (unsigned)align)
-      return zs::fail(ZS_ERR_ALIGN, "%s: %s is not %d-byte aligned", fn_, name, align);
-    if (p) items_[n_++] = {name, (uintptr_t)p, (uintptr_t)p + (uint64_t)bytes, output};
-    return ZS_OK;
-  }
-  zs_status need(const char* name, const void* p, int64_t bytes, int align, bool output) {
-    if (!p) return zs::fail(ZS_ERR_INVAL, "%s: %s is NULL", fn_, name);
-    return add(name, p, bytes, align, output);
-  }
-  // in_place: the buffers named so may be one and the same.
-  zs_status check(const char* in_place_out, const char* in_place_in) const {
-    for (int a = 0; a < n_; ++a) {
-      if (!items_[a].output) continue;
-      for (int b = 0; b < n_; ++b) {
-        if (a == b || items_[a].lo >= items_[b].hi || items_[b].lo >= items_[a].hi) continue;
-        if (items_[a].name == in_place_out && items_[b].name == in_place_in &&
-            items_[a].lo == items_[b].lo && items_[a].hi == items_[b].hi)
-          continue;
-        return zs::fail(ZS_ERR_INVAL, "%s: %s overlaps %s", fn_, items_[a].name, items_[b].name);
-      }
-    }
-    for (int a = 0; a < n_; ++a)
-      if (zs_status st = zs::check_device_array(
-              (const void*)items_[a].lo, (int64_t)(items_[a].hi - items_[a].lo), fn_,
-              items_[a].name))
-        return st;
-    return ZS_OK;
-  }
-
- private:
-  struct Item {
-    const char* name;
-    uintptr_t lo, hi;
-    bool output;
-  };
-  const char* fn_;
-  Item items_[20];
-  int n_ = 0;
-};
-
 const char* const kLogits = "logits";
 const char* const kGrad = "d_logits";
-
-// The rows of one matrix: (rows - 1) * stride + vocab elements, kMaxExtent at most
-// (2^46 bytes of fp32, past any device's memory), so that no product of them wraps.
-constexpr int64_t kMaxExtent = int64_t(1) << 44;
-zs_status check_stride(const char* fn, const char* name, int64_t stride,
-                       const zs::VocabLaunch& a) {
-  if (stride < a.vocab || stride > int64_t(1) << 40)
-    return zs::fail(ZS_ERR_RANGE, "%s: %s %lld outside vocab..2^40", fn, name, (long long)stride);
-  if (a.rows > 1 && stride > (kMaxExtent - a.vocab) / (a.rows - 1))
-    return zs::fail(ZS_ERR_RANGE, "%s: %lld rows %s %lld apart are more than 2^44 elements", fn,
-                    (long long)a.rows, name, (long long)stride);
-  return ZS_OK;
-}
 
 // Sizes, dtype, stride and temperature.
 zs_status check_rows(const char* fn, const zs::VocabLaunch& a) {
@@ -79,9 +20,13 @@ zs_status check_rows(const char* fn, const zs::VocabLaunch& a) {
   if (a.vocab < 1 || a.vocab > ZS_MAX_VOCAB)
     return zs::fail(ZS_ERR_RANGE, "%s: vocab %lld outside 1..%d", fn, (long long)a.vocab,
                     ZS_MAX_VOCAB);
-  if (zs_status st = check_stride(fn, "row_stride", a.row_stride, a)) return st;
+  if (zs_status st =
+          zs::check_stride(fn, "row_stride", a.row_stride, a.rows, a.vocab, "vocab"))
+    return st;
   if (a.d_logits)
-    if (zs_status st = check_stride(fn, "grad_stride", a.grad_stride, a)) return st;
+    if (zs_status st =
+            zs::check_stride(fn, "grad_stride", a.grad_stride, a.rows, a.vocab, "vocab"))
+      return st;
   // (log2(e)/T is finite in fp32 and 1/T normal, and so is T times an lse of flat rows)
   if (!(a.temperature >= 1e-38 && a.temperature <= 1e37))
     return zs::fail(ZS_ERR_INVAL, "%s: temperature must be within 1e-38..1e37 (got %g)", fn,
@@ -93,7 +38,7 @@ zs_status check_rows(const char* fn, const zs::VocabLaunch& a) {
 zs_status check_buffers(const char* fn, const zs::VocabLaunch& a) {
   const int es = zs::elem_bytes(a.dtype);
   const int64_t R = a.rows;
-  Buffers b(fn);
+  zs::Buffers b(fn);
   if (zs_status st = b.need(kLogits, a.logits, ((R - 1) * a.row_stride + a.vocab) * es, es, false))
     return st;
   if (zs_status st = b.add("targets", a.targets, R * 8, 8, false)) return st;
@@ -125,7 +70,8 @@ zs_status check_buffers(const char* fn, const zs::VocabLaunch& a) {
   if (zs_status st = b.add(kGrad, a.d_logits, ((R - 1) * a.grad_stride + a.vocab) * es, es, true))
     return st;
   const bool in_place = a.d_logits && a.d_logits == a.logits && a.grad_stride == a.row_stride;
-  return b.check(in_place ? kGrad : nullptr, kLogits);
+  if (in_place) b.may_share(kGrad, kLogits);
+  return b.check();
 }
 
 zs_status check_teacher(const char* fn, const zs::VocabLaunch& a) {
@@ -135,12 +81,6 @@ zs_status check_teacher(const char* fn, const zs::VocabLaunch& a) {
   if (a.teacher_k > 0 && a.teacher_dtype != ZS_BF16 && a.teacher_dtype != ZS_FP32)
     return zs::fail(ZS_ERR_INVAL, "%s: teacher dtype %d is not bf16 or fp32", fn,
                     (int)a.teacher_dtype);
-  return ZS_OK;
-}
-
-zs_status launched(const char* fn, cudaError_t e) {
-  if (e != cudaSuccess)
-    return zs::fail(ZS_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
   return ZS_OK;
 }
 
@@ -192,7 +132,7 @@ extern "C" zs_status zs_token_logprobs(const void* logits, zs_dtype dtype, int64
   if (rows == 0) return ZS_OK;
   if (logprob && !targets) return zs::fail(ZS_ERR_INVAL, "%s: logprob needs targets", fn);
   if (zs_status st = check_buffers(fn, a)) return st;
-  return launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
+  return zs::launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 extern "C" zs_status zs_token_logprobs_grad(const void* logits, zs_dtype dtype, int64_t rows,
@@ -219,7 +159,7 @@ extern "C" zs_status zs_token_logprobs_grad(const void* logits, zs_dtype dtype, 
   if (d_logprob && !targets) return zs::fail(ZS_ERR_INVAL, "%s: d_logprob needs targets", fn);
   if (d_entropy && !entropy) return zs::fail(ZS_ERR_INVAL, "%s: d_entropy needs entropy", fn);
   if (zs_status st = check_buffers(fn, a)) return st;
-  return launched(fn, zs::launch_vocab_grad(a, static_cast<cudaStream_t>(cuda_stream)));
+  return zs::launched(fn, zs::launch_vocab_grad(a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 extern "C" zs_status zs_distill_loss(const void* logits, zs_dtype dtype, int64_t rows,
@@ -245,7 +185,7 @@ extern "C" zs_status zs_distill_loss(const void* logits, zs_dtype dtype, int64_t
   if (rows == 0) return ZS_OK;
   if (logprob && !targets) return zs::fail(ZS_ERR_INVAL, "%s: logprob needs targets", fn);
   if (zs_status st = check_buffers(fn, a)) return st;
-  return launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
+  return zs::launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 extern "C" zs_status zs_distill_grad(const void* logits, zs_dtype dtype, int64_t rows,
@@ -278,7 +218,7 @@ extern "C" zs_status zs_distill_grad(const void* logits, zs_dtype dtype, int64_t
   if (d_logprob && (!targets || !hard_lse))
     return zs::fail(ZS_ERR_INVAL, "%s: d_logprob needs targets and hard_lse", fn);
   if (zs_status st = check_buffers(fn, a)) return st;
-  return launched(fn, zs::launch_vocab_grad(a, static_cast<cudaStream_t>(cuda_stream)));
+  return zs::launched(fn, zs::launch_vocab_grad(a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 extern "C" zs_status zs_distill_loss_grad(const void* logits, zs_dtype dtype, int64_t rows,
@@ -313,5 +253,5 @@ extern "C" zs_status zs_distill_loss_grad(const void* logits, zs_dtype dtype, in
   if ((d_logprob || logprob) && !targets)
     return zs::fail(ZS_ERR_INVAL, "%s: logprob and d_logprob need targets", fn);
   if (zs_status st = check_buffers(fn, a)) return st;
-  return launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
+  return zs::launched(fn, zs::launch_vocab_loss(a, static_cast<cudaStream_t>(cuda_stream)));
 }

@@ -176,6 +176,63 @@ cudaError_t launch_vocab_loss(const VocabLaunch& a, cudaStream_t stream);
 // The gradient from the forward call's normalisers.
 cudaError_t launch_vocab_grad(const VocabLaunch& a, cudaStream_t stream);
 
+// The operators around the layers (embedding.cu, layer_norm.cu, tensors.cu); the
+// entry points are in layers_api.cpp. A call fills what it uses and leaves the
+// rest zero; the launchers assume validated input.
+struct EmbeddingLaunch {
+  const void* table;       // lookup: vocab x dim
+  zs_dtype table_dtype;    // of table, add and d_table
+  int64_t vocab, dim, table_stride;
+  const int64_t* tokens;
+  int64_t rows;
+  double scale;
+  void* rows_out;          // lookup
+  const void* rows_in;     // gradient: d_out
+  zs_dtype dtype;          // of rows_out, rows_in
+  int64_t row_stride;
+  const void* add;         // gradient: what the sums are added to (d_table itself, another, NULL)
+  void* d_table;
+  void* workspace;
+};
+cudaError_t launch_embedding(const EmbeddingLaunch& a, cudaStream_t stream);
+cudaError_t launch_embedding_grad(const EmbeddingLaunch& a, cudaStream_t stream);
+int64_t embedding_grad_workspace_bytes(int64_t rows, int64_t dim);
+
+struct LayerNormLaunch {
+  const void *x, *residual;
+  zs_dtype dtype;
+  int64_t rows, dim, row_stride, out_stride, grad_stride;
+  const void *weight, *bias;
+  zs_dtype weight_dtype, grad_dtype;
+  double eps;
+  void *sum, *y;
+  float *mean, *rstd;      // written by the forward pass, read by the backward pass
+  const void *d_y, *d_sum;
+  void* d_x;
+  void *d_weight, *d_bias;
+  void* workspace;
+};
+cudaError_t launch_layer_norm(const LayerNormLaunch& a, cudaStream_t stream);
+cudaError_t launch_layer_norm_grad(const LayerNormLaunch& a, cudaStream_t stream);
+int64_t layer_norm_grad_workspace_bytes(int64_t rows, int64_t dim);
+
+struct TensorsLaunch {
+  const void* const* tensors;  // host arrays
+  const int64_t* numels;
+  void* const* outs;
+  int64_t count;
+  zs_dtype dtype, out_dtype;
+  void* workspace;         // kNormWorkspaceBytes
+  double* sqnorm;
+  double max_norm;         // 0: the sum of squares alone
+  float *norm, *coef_out;
+  int32_t* nonfinite_out;
+  const float* coef;       // of the scaling
+  const int32_t* skip;
+};
+// The norm (and with max_norm the coefficient), then the scaling.
+cudaError_t launch_tensors(const TensorsLaunch& a, bool norm, bool scale, cudaStream_t stream);
+
 // Argument checks of the C-ABI layer, for the other host translation units:
 // device-resident on the current device and (where the driver can tell)
 // [p, p + bytes) inside one allocation.

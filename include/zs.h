@@ -40,6 +40,8 @@ extern "C" {
 #define ZS_MAX_VOCAB 1048576 /* columns of a row of logits */
 #define ZS_MAX_TOP 128       /* top alternatives of a token */
 #define ZS_MAX_TEACHER 256   /* entries of a teacher's record for a token */
+#define ZS_MAX_DIM 32768     /* columns of a row of hidden values */
+#define ZS_MAX_TENSORS 65536 /* gradients of one list */
 
 typedef enum {
   ZS_OK = 0,
@@ -571,6 +573,132 @@ zs_status zs_distill_loss_grad(const void* logits, zs_dtype dtype, int64_t rows,
                                const float* d_logprob, float* loss, float* lse, float* logprob,
                                float* hard_lse, void* d_logits, int64_t grad_stride,
                                void* cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the layers: what a training step runs before its losses and behind its
+ * backward pass, next to the matrix products. The pages take all of it as given
+ * and have no counterpart.
+ *
+ * Common arguments:
+ *   rows              tokens of a batch, 0..2^31-1; dim columns, 1..ZS_MAX_DIM.
+ *                     A matrix's row r starts at element r * its stride (stride
+ *                     >= dim, up to 2^40, (rows - 1) * stride + dim up to 2^44).
+ *                     Only the type's own alignment is needed (so a view of the
+ *                     flat parameter buffer will do), but for workspaces, which
+ *                     are 16-byte aligned and used by one call at a time; rows
+ *                     that start on 16-byte boundaries are the fast ones.
+ *                     Elements between dim and the strides are not touched.
+ *   dtypes            ZS_BF16 or ZS_FP32. Statistics and sums are fp32 (the
+ *                     norm's in double); a result is rounded once, to nearest
+ *                     even. Results do not depend on timing: the same call gives
+ *                     the same bits.
+ * An output may not overlap another buffer of the call (a matrix counts from its
+ * first element to its last), but where "in place" says so: then both begin at
+ * one address, with one stride. Errors: ZS_ERR_INVAL (NULL, dtype, overlap, not
+ * device memory), ZS_ERR_RANGE (sizes, a short workspace), ZS_ERR_ALIGN,
+ * ZS_ERR_CUDA.
+ *
+ * zs_embedding — the table's rows of given tokens: out_r = scale * table[tok_r].
+ *   table             vocab x dim of table_dtype; vocab 1..ZS_MAX_VOCAB.
+ *   tokens            int64 [rows]. A negative id (padding) gives a row of zeros;
+ *                     an id >= vocab a row of NaN, and it sets the device error
+ *                     word (zs_check_device_error: ZS_ERR_RANGE).
+ *   scale             finite in fp32.
+ *   out               rows x dim of out_dtype. With rows == 0 the call succeeds
+ *                     and touches nothing. */
+zs_status zs_embedding(const void* table, zs_dtype table_dtype, int64_t vocab, int64_t dim,
+                       int64_t table_stride, const int64_t* tokens, int64_t rows, double scale,
+                       void* out, zs_dtype out_dtype, int64_t out_stride, void* cuda_stream);
+/* Bytes of scratch device memory zs_embedding_grad needs (-1: sizes out of
+ * range). */
+int64_t zs_embedding_grad_workspace_bytes(int64_t rows, int64_t dim);
+/* zs_embedding_grad — the table's gradient:
+ *   d_table[v] = add_to[v] + scale * sum over r with tok_r = v of d_out_r
+ * the sum in the order of the tokens (runs of over 64 in parts). Ids outside the
+ * vocabulary have no row; one >= vocab sets the device error word.
+ *   add_to            NULL (zero), or vocab x dim of table_dtype with d_table's
+ *                     stride: another gradient of the same table (a tied head's,
+ *                     an earlier micro-batch's). In place (d_table itself): only
+ *                     the rows of the batch's tokens are touched.
+ *   d_table           every row is written otherwise, with rows == 0 too. */
+zs_status zs_embedding_grad(const void* d_out, zs_dtype dtype, int64_t rows, int64_t dim,
+                            int64_t row_stride, const int64_t* tokens, int64_t vocab,
+                            double scale, const void* add_to, void* workspace,
+                            int64_t workspace_bytes, void* d_table, zs_dtype table_dtype,
+                            int64_t table_stride, void* cuda_stream);
+/* zs_layer_norm — layer norm of each row, behind a residual sum if one is given:
+ *   h = x + residual, rounded to dtype         (h = x without a residual)
+ *   y = (h - mean) * rstd * weight + bias,     rstd = 1 / sqrt(var + eps)
+ * with mean and var (the mean squared deviation) of the row's dim values of h.
+ *   x, residual       rows x dim of dtype, row_stride apart; residual may be NULL.
+ *   weight, bias      [dim] of weight_dtype; NULL: 1 and 0.
+ *   eps               1e-30..1e30.
+ *   sum_out           NULL, or h (needs a residual), and
+ *   y                 rows x dim of dtype, out_stride apart. Each may be x or the
+ *                     residual in place.
+ *   mean, rstd        fp32 [rows] for the backward pass; either may be NULL.
+ * A NaN or an infinity makes its row NaN. Deviations up to 1e18 have squares that
+ * fp32 sums; past them a row's results are not defined. rows == 0: nothing. */
+zs_status zs_layer_norm(const void* x, zs_dtype dtype, int64_t rows, int64_t dim,
+                        int64_t row_stride, const void* residual, const void* weight,
+                        const void* bias, zs_dtype weight_dtype, double eps, void* sum_out,
+                        void* y, int64_t out_stride, float* mean, float* rstd,
+                        void* cuda_stream);
+/* Bytes of scratch device memory zs_layer_norm_grad needs for d_weight and d_bias
+ * (-1: sizes out of range). */
+int64_t zs_layer_norm_grad_workspace_bytes(int64_t rows, int64_t dim);
+/* zs_layer_norm_grad — its backward pass: with xh = (x - mean) * rstd, g = d_y *
+ * weight and averages over a row's dim values,
+ *   d_x = rstd * (g - avg(g) - xh * avg(g * xh)) + d_sum
+ *   d_weight = sum over rows of d_y * xh,  d_bias = sum over rows of d_y
+ *   x                 what was normalised (sum_out where there was a residual;
+ *                     d_x is then the gradient of x and of the residual alike),
+ *                     row_stride apart.
+ *   d_y, d_sum, d_x   rows x dim of dtype, grad_stride apart. d_sum: NULL, or the
+ *                     gradient that reaches h past the norm. d_x may be d_y or
+ *                     d_sum in place.
+ *   mean, rstd        as the forward call left them.
+ *   d_weight, d_bias  [dim] of grad_dtype; either may be NULL (with both, no
+ *                     workspace is needed). With rows == 0 they are zero. */
+zs_status zs_layer_norm_grad(const void* d_y, const void* x, zs_dtype dtype, int64_t rows,
+                             int64_t dim, int64_t grad_stride, int64_t row_stride,
+                             const void* weight, zs_dtype weight_dtype, const float* mean,
+                             const float* rstd, const void* d_sum, void* workspace,
+                             int64_t workspace_bytes, void* d_x, void* d_weight, void* d_bias,
+                             zs_dtype grad_dtype, void* cuda_stream);
+/* The norm and the clipping of gradients that are still tensors of their own
+ * (before they are flattened, or where each parameter is sharded by itself); the
+ * counterpart of zs_grad_sqnorm, which takes a flat shard's slices.
+ *   tensors, numels   host arrays of n device pointers and lengths, n 0..
+ *                     ZS_MAX_TENSORS; lengths 0..2^44, their sum too (a tensor
+ *                     of length 0 may be NULL). All of one dtype: gradients of
+ *                     two types make two lists, whose sums zs_clip_coefficient
+ *                     joins (as it joins the ranks'). The arrays are read before
+ *                     the call returns.
+ *   workspace         zs_grad_norm_workspace_bytes() bytes.
+ *
+ * zs_tensors_sqnorm — *sqnorm_out (device double) = the sum of all squares, each
+ * fp32 group of 8 added in double; squares past fp32's range are summed in double
+ * throughout. */
+zs_status zs_tensors_sqnorm(const void* const* tensors, const int64_t* numels, int32_t n,
+                            zs_dtype dtype, void* workspace, int64_t workspace_bytes,
+                            double* sqnorm_out, void* cuda_stream);
+/* zs_tensors_scale — outs[i] = tensors[i] * (*coef), in out_dtype; nothing when
+ * skip is not NULL and *skip != 0. coef and skip are device pointers, as
+ * zs_clip_coefficient leaves them. outs[i] may be tensors[i] in place (of the same
+ * dtype), or lie anywhere else: in a flat gradient buffer, say. */
+zs_status zs_tensors_scale(const void* const* tensors, const int64_t* numels, int32_t n,
+                           zs_dtype dtype, const float* coef, const int32_t* skip,
+                           void* const* outs, zs_dtype out_dtype, void* cuda_stream);
+/* zs_tensors_clip — both, for gradients that one rank holds whole, with the
+ * coefficient between them: *norm_out = sqrt(sum of squares), *coef_out = fp32(min(1,
+ * max_norm / (norm + 1e-6))), *nonfinite_out = !isfinite(norm), all on the device;
+ * a norm that is not finite leaves the outs as they are (and *coef_out = 1).
+ * max_norm: finite, > 0. */
+zs_status zs_tensors_clip(const void* const* tensors, const int64_t* numels, int32_t n,
+                          zs_dtype dtype, double max_norm, void* const* outs, zs_dtype out_dtype,
+                          void* workspace, int64_t workspace_bytes, float* norm_out,
+                          float* coef_out, int32_t* nonfinite_out, void* cuda_stream);
 
 /* Diagnostics. */
 const char* zs_status_string(zs_status status);
