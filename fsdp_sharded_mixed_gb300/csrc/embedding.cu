@@ -40,7 +40,7 @@ struct LookupArgs {
 // A warp to a row and kAtOnce slabs of it.
 constexpr int kAtOnce = 4;
 
-template <typename TT, typename OT, bool VEC>
+template <typename TT, typename OT, Lay LAY>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_constant__ LookupArgs a) {
   overlap_wait();
   const int64_t row = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
@@ -55,19 +55,19 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
 #pragma unroll
     for (int k = 0; k < kLane; ++k) v[k] = token < 0 ? 0.0f : NAN;
 #pragma unroll
-    for (int s = 0; s < kAtOnce; ++s) store8<OT, VEC>(out, col0 + s * kSlab, lane, a.dim, v);
+    for (int s = 0; s < kAtOnce; ++s) store8<OT, LAY>(out, col0 + s * kSlab, lane, a.dim, v);
     return;
   }
   const TT* from = static_cast<const TT*>(a.table) + token * a.table_stride;
   Raw8<TT> r[kAtOnce];
 #pragma unroll
-  for (int s = 0; s < kAtOnce; ++s) r[s] = load8<TT, VEC>(from, col0 + s * kSlab, lane, a.dim);
+  for (int s = 0; s < kAtOnce; ++s) r[s] = load8<TT, LAY>(from, col0 + s * kSlab, lane, a.dim);
 #pragma unroll
   for (int s = 0; s < kAtOnce; ++s) {
     float v[kLane];
 #pragma unroll
     for (int k = 0; k < kLane; ++k) v[k] = raw_value(r[s], k) * a.scale;
-    store8<OT, VEC>(out, col0 + s * kSlab, lane, a.dim, v);
+    store8<OT, LAY>(out, col0 + s * kSlab, lane, a.dim, v);
   }
 }
 
@@ -177,7 +177,7 @@ struct GradArgs {
 };
 
 // Every row: zero, or what the gradient is added to.
-template <typename GT, bool VEC>
+template <typename GT, Lay LAY>
 __global__ void __launch_bounds__(kThreads) fill_rows_kernel(const __grid_constant__ GradArgs a) {
   overlap_wait();
   const int lane = threadIdx.x & 31;
@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(kThreads) fill_rows_kernel(const __grid_consta
   for (int col0 = 0; col0 < a.dim; col0 += kSlab) {
     float x[kLane];
     Raw8<GT> r;
-    if (add) r = load8<GT, VEC>(add, col0, lane, a.dim);
+    if (add) r = load8<GT, LAY>(add, col0, lane, a.dim);
 #pragma unroll
     for (int k = 0; k < kLane; ++k) x[k] = add ? raw_value(r, k) : 0.0f;
-    store8<GT, VEC>(row, col0, lane, a.dim, x);
+    store8<GT, LAY>(row, col0, lane, a.dim, x);
   }
 }
 
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) fill_rows_kernel(const __grid_consta
 constexpr int kBlock = 32;    // sorted positions of a warp
 constexpr int kLongRun = 64;  // equal tokens that one warp sums by itself
 
-template <typename T, typename GT, bool VEC>
+template <typename T, typename GT, Lay LAY>
 struct Reduce {
   const GradArgs& a;
   const int lane, col0;
@@ -215,7 +215,7 @@ struct Reduce {
   }
   __device__ __forceinline__ Raw8<T> row(uint32_t t) {
     if (!within(t, (int64_t)t + 1, 0, a.rows, a.err)) t = 0;
-    return load8<T, VEC>(static_cast<const T*>(a.d_out) + (int64_t)t * a.row_stride, col0, lane,
+    return load8<T, LAY>(static_cast<const T*>(a.d_out) + (int64_t)t * a.row_stride, col0, lane,
                          a.dim);
   }
   // The rows of lanes [l, l + n) of `order`.
@@ -235,27 +235,27 @@ struct Reduce {
     const int64_t at = (int64_t)v * a.table_stride;
     float x[kLane];
     if (a.add) {
-      const Raw8<GT> r = load8<GT, VEC>(static_cast<const GT*>(a.add) + at, col0, lane, a.dim);
+      const Raw8<GT> r = load8<GT, LAY>(static_cast<const GT*>(a.add) + at, col0, lane, a.dim);
 #pragma unroll
       for (int k = 0; k < kLane; ++k) x[k] = __fmaf_rn(acc[k], a.scale, raw_value(r, k));
     } else {
 #pragma unroll
       for (int k = 0; k < kLane; ++k) x[k] = acc[k] * a.scale;
     }
-    store8<GT, VEC>(static_cast<GT*>(a.d_table) + at, col0, lane, a.dim, x);
+    store8<GT, LAY>(static_cast<GT*>(a.d_table) + at, col0, lane, a.dim, x);
   }
   // Parts are part_dim apart, a whole number of lanes: a lane finds its elements
   // where it left them, in either order of columns.
   __device__ __forceinline__ void write_part(int64_t slot) {
     if (!within(slot, slot + 1, 0, 2 * a.blocks, a.err)) return;
-    store8<float, VEC>(a.parts + slot * a.part_dim, col0, lane, a.part_dim, acc);
+    store8<float, LAY>(a.parts + slot * a.part_dim, col0, lane, a.part_dim, acc);
   }
   __device__ __forceinline__ void add_part(int64_t slot) {
     if (!within(slot, slot + 1, 0, 2 * a.blocks, a.err)) return;
     const float* p = a.parts + slot * a.part_dim;
 #pragma unroll
     for (int k = 0; k < kLane; ++k) {
-      const int c = column<VEC>(col0, lane, k);
+      const int c = column<LAY>(col0, lane, k);
       if (c < a.part_dim) acc[k] = __fadd_rn(acc[k], __ldcg(p + c));
     }
   }
@@ -274,7 +274,7 @@ __device__ __forceinline__ int64_t lower_bound(const GradArgs& a, uint32_t v, in
   return lo;
 }
 
-template <typename T, typename GT, bool VEC>
+template <typename T, typename GT, Lay LAY>
 __global__ void __launch_bounds__(kThreads) sum_tokens_kernel(const __grid_constant__ GradArgs a) {
   overlap_wait();
   const int lane = threadIdx.x & 31;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) sum_tokens_kernel(const __grid_const
   const uint32_t before2 = key_at(p - 64), before = key_at(p - 32), here = key_at(p),
                  after = key_at(p + 32), after2 = key_at(p + 64);
   const uint32_t order = order_at(p), order1 = order_at(p + 32), order2 = order_at(p + 64);
-  Reduce<T, GT, VEC> r{a, lane, (int)blockIdx.y * kSlab, {}};
+  Reduce<T, GT, LAY> r{a, lane, (int)blockIdx.y * kSlab, {}};
   for (int l = 0; l < kBlock;) {
     const uint32_t v = __shfl_sync(none, here, l);
     if (v >= (uint32_t)a.vocab) return;  // the tokens without a row, and the end
@@ -334,19 +334,19 @@ template <typename TT, typename OT>
 cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.rows + kWarps - 1) / kWarps),
                   (unsigned)((a.dim + kAtOnce * kSlab - 1) / (kAtOnce * kSlab)));
-  return vec ? launch_kernel(embedding_kernel<TT, OT, true>, grid, dim3(kThreads), 0, stream, a)
-             : launch_kernel(embedding_kernel<TT, OT, false>, grid, dim3(kThreads), 0, stream, a);
+  return vec ? launch_kernel(embedding_kernel<TT, OT, kEight>, grid, dim3(kThreads), 0, stream, a)
+             : launch_kernel(embedding_kernel<TT, OT, kOne>, grid, dim3(kThreads), 0, stream, a);
 }
 
-template <typename T, typename GT, bool VEC>
+template <typename T, typename GT, Lay LAY>
 cudaError_t launch_sums(const GradArgs& a, bool fill, bool sums, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (fill)
-    e = launch_kernel(fill_rows_kernel<GT, VEC>, dim3((unsigned)((a.vocab + kWarps - 1) / kWarps)),
+    e = launch_kernel(fill_rows_kernel<GT, LAY>, dim3((unsigned)((a.vocab + kWarps - 1) / kWarps)),
                       dim3(kThreads), 0, stream, a);
   if (e != cudaSuccess || !sums) return e;
   const dim3 grid((unsigned)((a.blocks + kWarps - 1) / kWarps), (unsigned)a.slabs);
-  return launch_kernel(sum_tokens_kernel<T, GT, VEC>, grid, dim3(kThreads), 0, stream, a);
+  return launch_kernel(sum_tokens_kernel<T, GT, LAY>, grid, dim3(kThreads), 0, stream, a);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -453,16 +453,16 @@ cudaError_t launch_embedding_grad(const EmbeddingLaunch& in, cudaStream_t stream
   const bool fill = a.add != a.d_table, sums = in.rows > 0;
   if (br) {
     if (bt)
-      return vec ? launch_sums<__nv_bfloat16, __nv_bfloat16, true>(a, fill, sums, stream)
-                 : launch_sums<__nv_bfloat16, __nv_bfloat16, false>(a, fill, sums, stream);
-    return vec ? launch_sums<__nv_bfloat16, float, true>(a, fill, sums, stream)
-               : launch_sums<__nv_bfloat16, float, false>(a, fill, sums, stream);
+      return vec ? launch_sums<__nv_bfloat16, __nv_bfloat16, kEight>(a, fill, sums, stream)
+                 : launch_sums<__nv_bfloat16, __nv_bfloat16, kOne>(a, fill, sums, stream);
+    return vec ? launch_sums<__nv_bfloat16, float, kEight>(a, fill, sums, stream)
+               : launch_sums<__nv_bfloat16, float, kOne>(a, fill, sums, stream);
   }
   if (bt)
-    return vec ? launch_sums<float, __nv_bfloat16, true>(a, fill, sums, stream)
-               : launch_sums<float, __nv_bfloat16, false>(a, fill, sums, stream);
-  return vec ? launch_sums<float, float, true>(a, fill, sums, stream)
-             : launch_sums<float, float, false>(a, fill, sums, stream);
+    return vec ? launch_sums<float, __nv_bfloat16, kEight>(a, fill, sums, stream)
+               : launch_sums<float, __nv_bfloat16, kOne>(a, fill, sums, stream);
+  return vec ? launch_sums<float, float, kEight>(a, fill, sums, stream)
+             : launch_sums<float, float, kOne>(a, fill, sums, stream);
 }
 
 }  // namespace zs

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) list_sqnorm_kernel(const __grid_cons
     const bool vec = (uintptr_t)p % 16 == 0;
     const int lane = threadIdx.x & 31;
     for (int col0 = threadIdx.x / 32 * kSlab; col0 < n; col0 += kThreads / 32 * kSlab) {
-      const Raw8<T> r = vec ? load8<T, true>(p, col0, lane, n) : load8<T, false>(p, col0, lane, n);
+      const Raw8<T> r = vec ? load8<T, kEight>(p, col0, lane, n) : load8<T, kOne>(p, col0, lane, n);
       float v[kLane];
 #pragma unroll
       for (int k = 0; k < kLane; ++k) v[k] = raw_value(r, k);
@@ -143,14 +143,14 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(const __grid_const
     const bool vec = ((uintptr_t)p | (uintptr_t)q) % 16 == 0;
     const int lane = threadIdx.x & 31;
     for (int col0 = threadIdx.x / 32 * kSlab; col0 < n; col0 += kThreads / 32 * kSlab) {
-      const Raw8<T> r = vec ? load8<T, true>(p, col0, lane, n) : load8<T, false>(p, col0, lane, n);
+      const Raw8<T> r = vec ? load8<T, kEight>(p, col0, lane, n) : load8<T, kOne>(p, col0, lane, n);
       float v[kLane];
 #pragma unroll
       for (int k = 0; k < kLane; ++k) v[k] = raw_value(r, k) * coef;
       if (vec)
-        store8<OT, true>(q, col0, lane, n, v);
+        store8<OT, kEight>(q, col0, lane, n, v);
       else
-        store8<OT, false>(q, col0, lane, n, v);
+        store8<OT, kOne>(q, col0, lane, n, v);
     }
   }
 }
