@@ -71,98 +71,22 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const __grid_consta
   }
 }
 
-// ---- the tokens sorted ----------------------------------------------------------
+// ---- the tokens sorted, the other rows written ------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortBlocks = 8;  // one cluster (the portable size)
 constexpr int kMaxDigits = 1024;
+constexpr int kAtHand = 4;      // rounds of a warp's tokens on their way at once
 
 struct SortArgs {
   const int64_t* tokens;
   uint32_t *keys, *order;    // sorted: the row of the table, and which token it was
   uint32_t *keys2, *order2;  // between passes
   uint32_t* tickets;         // cleared for the reduction
-  int64_t rows, n_tickets;
+  int64_t rows, n_tickets, share;  // share: tokens of a warp
   int32_t vocab, passes, bits;
-  unsigned int* err;
 };
 
-// Tokens without a row (negative, or past the vocabulary, which sets the error
-// word) get the key `vocab` and come last.
-__device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
-  const int64_t token = a.tokens[i];
-  if (token >= 0 && token < a.vocab) return (uint32_t)token;
-  if (token >= 0) atomicOr(a.err, 4u);
-  return (uint32_t)a.vocab;
-}
-
-// One block; each warp keeps its share of the tokens in order. A pass counts
-// the digits warp by warp, turns the counts into places (digit first, then
-// warp) and moves each warp's tokens to theirs, 32 at a time.
-__global__ void __launch_bounds__(kSortThreads, 1) sort_tokens_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ uint32_t hist[];  // [kSortWarps][digits]
-  __shared__ uint32_t warp_total[kSortWarps];
-  overlap_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-  const int digits = 1 << a.bits;
-  const int64_t share = ((a.rows + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-  const int64_t lo = min(a.rows, share * warp), hi = min(a.rows, share * (warp + 1));
-  for (int64_t i = tid; i < a.n_tickets; i += kSortThreads) a.tickets[i] = 0;
-  uint32_t* mine = hist + warp * digits;
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int shift = pass * a.bits;
-    // the last pass ends in keys, order
-    const bool to_first = (a.passes - 1 - pass) % 2 == 0;
-    const uint32_t* ks = to_first ? a.keys2 : a.keys;
-    const uint32_t* os = to_first ? a.order2 : a.order;
-    uint32_t* kd = to_first ? a.keys : a.keys2;
-    uint32_t* od = to_first ? a.order : a.order2;
-    for (int i = tid; i < kSortWarps * digits; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-      const uint32_t key = pass == 0 ? key_of(a, i) : ks[i];
-      atomicAdd(&mine[(key >> shift) & (digits - 1)], 1u);
-    }
-    __syncthreads();
-    uint32_t total = 0;
-    if (tid < digits)
-      for (int w = 0; w < kSortWarps; ++w) total += hist[w * digits + tid];
-    uint32_t upto = total;  // inclusive, over the warp's digits
-    for (int off = 1; off < 32; off *= 2) {
-      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, off);
-      if (lane >= off) upto += x;
-    }
-    if (lane == 31) warp_total[warp] = upto;
-    __syncthreads();
-    uint32_t at = upto - total;
-    for (int w = 0; w < warp; ++w) at += warp_total[w];
-    if (tid < digits)
-      for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t n = hist[w * digits + tid];
-        hist[w * digits + tid] = at;
-        at += n;
-      }
-    __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool some = i < hi;
-      const uint32_t key = !some ? 0 : pass == 0 ? key_of(a, i) : ks[i];
-      const uint32_t from = !some ? 0 : pass == 0 ? (uint32_t)i : os[i];
-      const uint32_t digit = some ? (key >> shift) & (digits - 1) : 0xFFFFFFFFu;
-      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
-      const uint32_t place = some ? mine[digit] + __popc(peers & ((1u << lane) - 1)) : 0;
-      __syncwarp();
-      if (some && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
-      __syncwarp();
-      if (some && within(place, (int64_t)place + 1, 0, a.rows, a.err)) {
-        kd[place] = key;
-        od[place] = from;
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// ---- rows without tokens ---------------------------------------------------------
 struct GradArgs {
   const void* d_out;
   const void* add;    // or NULL
@@ -176,23 +100,169 @@ struct GradArgs {
   unsigned int* err;
 };
 
-// Every row: zero, or what the gradient is added to.
-template <typename GT, Lay LAY>
-__global__ void __launch_bounds__(kThreads) fill_rows_kernel(const __grid_constant__ GradArgs a) {
-  overlap_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t v = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  if (v >= a.vocab || !within(v, v + 1, 0, a.vocab, a.err)) return;
-  GT* row = static_cast<GT*>(a.d_table) + v * a.table_stride;
-  const GT* add = a.add ? static_cast<const GT*>(a.add) + v * a.table_stride : nullptr;
-  for (int col0 = 0; col0 < a.dim; col0 += kSlab) {
-    float x[kLane];
-    Raw8<GT> r;
-    if (add) r = load8<GT, LAY>(add, col0, lane, a.dim);
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// A word of another block's shared memory, at the place of this block's p.
+__device__ __forceinline__ uint32_t word_of(const uint32_t* p, int rank) {
+  uint32_t at = (uint32_t)__cvta_generic_to_shared(p), x;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+// Tokens without a row (negative, or past the vocabulary, which sets the error
+// word) get the key `vocab` and come last.
+__device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i, unsigned int* err) {
+  const int64_t token = a.tokens[i];
+  if (token >= 0 && token < a.vocab) return (uint32_t)token;
+  if (token >= 0) atomicOr(err, 4u);
+  return (uint32_t)a.vocab;
+}
+
+// A stable counting sort by digits, the lowest first, by the kSortBlocks blocks of
+// one cluster; each warp keeps its share of the tokens in order. A pass counts the
+// digits warp by warp, turns the counts into places (by digit, then block, then
+// warp) and moves each warp's tokens to theirs, 32 at a time.
+struct SortShared {
+  uint32_t of_block[kMaxDigits];    // the block's counts, read by the others
+  uint32_t of_warp[kSortWarps];
+  uint32_t count[1];                // [kSortWarps][digits]
+};
+__device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigned int* err) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const int digits = 1 << a.bits;
+  const int64_t lo = min(a.rows, a.share * (rank * kSortWarps + warp));
+  const int64_t hi = min(a.rows, lo + a.share);
+  for (int64_t i = rank * kSortThreads + tid; i < a.n_tickets; i += kSortBlocks * kSortThreads)
+    a.tickets[i] = 0;
+  uint32_t* mine = sh.count + warp * digits;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    // the last pass ends in keys, order
+    const bool to_first = (a.passes - 1 - pass) % 2 == 0;
+    const uint32_t* ks = to_first ? a.keys2 : a.keys;
+    const uint32_t* os = to_first ? a.order2 : a.order;
+    uint32_t* kd = to_first ? a.keys : a.keys2;
+    uint32_t* od = to_first ? a.order : a.order2;
+    for (int i = tid; i < kSortWarps * digits; i += kSortThreads) sh.count[i] = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int64_t i = lo + lane; i < hi; i += 32) {
+      const uint32_t key = pass == 0 ? key_of(a, i, err) : __ldcg(ks + i);
+      atomicAdd(&mine[(key >> shift) & (digits - 1)], 1u);
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    if (tid < digits) {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) x[k] = add ? raw_value(r, k) : 0.0f;
-    store8<GT, LAY>(row, col0, lane, a.dim, x);
+      for (int w = 0; w < kSortWarps; ++w) total += sh.count[w * digits + tid];
+      sh.of_block[tid] = total;
+    }
+    cluster_sync();
+    uint32_t all = 0, before = 0;
+    if (tid < digits)
+#pragma unroll
+      for (int r = 0; r < kSortBlocks; ++r) {
+        const uint32_t n = word_of(sh.of_block + tid, r);
+        before += r < rank ? n : 0;
+        all += n;
+      }
+    uint32_t upto = all;  // inclusive, over the warp's digits
+    for (int off = 1; off < 32; off *= 2) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    if (lane == 31) sh.of_warp[warp] = upto;
+    __syncthreads();
+    const uint32_t ahead = lane < warp ? sh.of_warp[lane] : 0;
+    uint32_t at = upto - all + before + __reduce_add_sync(0xFFFFFFFFu, ahead);
+    if (tid < digits) {
+#pragma unroll 8
+      for (int w = 0; w < kSortWarps; ++w) {
+        const uint32_t n = sh.count[w * digits + tid];
+        sh.count[w * digits + tid] = at;
+        at += n;
+      }
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAtHand) {
+      uint32_t keys[kAtHand], from[kAtHand];
+#pragma unroll
+      for (int u = 0; u < kAtHand; ++u) {
+        const int64_t i = i0 + u * 32 + lane;
+        const bool some = i < hi;
+        keys[u] = !some ? 0 : pass == 0 ? key_of(a, i, err) : __ldcg(ks + i);
+        from[u] = !some ? 0 : pass == 0 ? (uint32_t)i : __ldcg(os + i);
+      }
+#pragma unroll
+      for (int u = 0; u < kAtHand; ++u) {
+        if (i0 + u * 32 >= hi) break;
+        const bool some = i0 + u * 32 + lane < hi;
+        const uint32_t digit = some ? (keys[u] >> shift) & (digits - 1) : 0xFFFFFFFFu;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
+        const uint32_t place = some ? mine[digit] + __popc(peers & ((1u << lane) - 1)) : 0;
+        __syncwarp();
+        if (some && lane == __ffs(peers) - 1) mine[digit] += __popc(peers);
+        __syncwarp();
+        if (some && within(place, (int64_t)place + 1, 0, a.rows, err)) {
+          kd[place] = keys[u];
+          od[place] = from[u];
+        }
+      }
+    }
+    cluster_sync();  // what was moved is there for all, and the counts have been read
   }
+}
+
+// Rows of the table: zero, or what the gradient is added to.
+constexpr int kFillBytes = 32 * 1024;  // of a dense table, a block at a time
+template <typename GT, Lay LAY>
+__device__ void fill_rows(const GradArgs& a, int64_t block, int64_t blocks) {
+  const int lane = threadIdx.x & 31;
+  if (LAY != kOne && a.table_stride == a.dim && ((uintptr_t)a.d_table | (uintptr_t)a.add) % 32 == 0) {
+    // dense: 32 bytes a thread
+    const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT), whole = bytes / 32 * 32;
+    unsigned char* to = static_cast<unsigned char*>(a.d_table);
+    const unsigned char* from = static_cast<const unsigned char*>(a.add);
+    for (int64_t i = block * kFillBytes + threadIdx.x * 32; i < whole;
+         i += blocks * kFillBytes) {
+      if (!within(i, i + 32, 0, bytes, a.err)) continue;
+      uint32_t w[8] = {};
+      if (from) load_words<8>(w, from + i);
+      store_words<8>(to + i, w);
+    }
+    for (int64_t i = whole + threadIdx.x * (int)sizeof(GT); block == 0 && i < bytes;
+         i += kSortThreads * (int)sizeof(GT)) {
+      const GT* p = reinterpret_cast<const GT*>(from + i);
+      *reinterpret_cast<GT*>(to + i) = from ? *p : GT(0.0f);
+    }
+    return;
+  }
+  for (int64_t v = block * kSortWarps + threadIdx.x / 32; v < a.vocab; v += blocks * kSortWarps) {
+    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
+    GT* row = static_cast<GT*>(a.d_table) + v * a.table_stride;
+    const GT* add = a.add ? static_cast<const GT*>(a.add) + v * a.table_stride : nullptr;
+    for (int col0 = 0; col0 < a.dim; col0 += kSlab) {
+      Raw8<GT> r = {};
+      if (add) r = load8<GT, LAY>(add, col0, lane, a.dim);
+      store_raw8<GT, LAY>(row, col0, lane, a.dim, r);
+    }
+  }
+}
+
+// The first cluster sorts the tokens (where there are any); the others write the
+// rows meanwhile, those of the batch's tokens too, which the sums write again.
+template <typename GT, Lay LAY>
+__global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks, 1, 1)
+    sort_and_fill_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ GradArgs g) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  overlap_wait();
+  const int sorting = a.rows > 0 ? kSortBlocks : 0;
+  if ((int)blockIdx.x < sorting)
+    sort_tokens(a, *reinterpret_cast<SortShared*>(smem), (int)blockIdx.x, g.err);
+  else
+    fill_rows<GT, LAY>(g, (int64_t)blockIdx.x - sorting, (int64_t)gridDim.x - sorting);
 }
 
 // ---- sums over sorted tokens -----------------------------------------------------
@@ -201,62 +271,74 @@ constexpr int kLongRun = 64;  // equal tokens that one warp sums by itself
 
 template <typename T, typename GT, Lay LAY>
 struct Reduce {
+  static constexpr int kRows = 16 / (int)sizeof(T);  // on their way at once
   const GradArgs& a;
   const int lane, col0;
-  float acc[kLane];
+  float2 acc[kLane / 2];
+  Raw8<GT> base;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) acc[k] = 0.0f;
+    for (int i = 0; i < kLane / 2; ++i) acc[i] = {0.0f, 0.0f};
   }
   __device__ __forceinline__ void add(const Raw8<T>& r) {
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) acc[k] = __fadd_rn(acc[k], raw_value(r, k));
+    for (int i = 0; i < kLane / 2; ++i) acc[i] = __fadd2_rn(acc[i], pair_of(r, i));
   }
-  __device__ __forceinline__ Raw8<T> row(uint32_t t) {
+  __device__ __forceinline__ Raw8<T> row(uint32_t t) const {
     if (!within(t, (int64_t)t + 1, 0, a.rows, a.err)) t = 0;
     return load8<T, LAY>(static_cast<const T*>(a.d_out) + (int64_t)t * a.row_stride, col0, lane,
                          a.dim);
   }
-  // The rows of lanes [l, l + n) of `order`.
-  __device__ __forceinline__ void add_rows(uint32_t order, int l, int n) {
-    int i = 0;
-    for (; i + 4 <= n; i += 4) {
-      Raw8<T> r[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) r[u] = row(__shfl_sync(0xFFFFFFFFu, order, l + i + u));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) add(r[u]);
-    }
-    for (; i < n; ++i) add(row(__shfl_sync(0xFFFFFFFFu, order, l + i)));
+  __device__ __forceinline__ Raw8<GT> base_of(uint32_t v) const {
+    if (!within(v, (int64_t)v + 1, 0, a.vocab, a.err)) v = 0;
+    return load8<GT, LAY>(static_cast<const GT*>(a.add) + (int64_t)v * a.table_stride, col0, lane,
+                          a.dim);
   }
-  __device__ __forceinline__ void write(uint32_t v) {
+  __device__ __forceinline__ void write(uint32_t v) const {
     if (!within(v, (int64_t)v + 1, 0, a.vocab, a.err)) return;
-    const int64_t at = (int64_t)v * a.table_stride;
-    float x[kLane];
-    if (a.add) {
-      const Raw8<GT> r = load8<GT, LAY>(static_cast<const GT*>(a.add) + at, col0, lane, a.dim);
+    Raw8<GT> r;
 #pragma unroll
-      for (int k = 0; k < kLane; ++k) x[k] = __fmaf_rn(acc[k], a.scale, raw_value(r, k));
-    } else {
-#pragma unroll
-      for (int k = 0; k < kLane; ++k) x[k] = acc[k] * a.scale;
+    for (int i = 0; i < kLane / 2; ++i) {
+      const float2 scale = {a.scale, a.scale};
+      set_pair(r, i, a.add ? __ffma2_rn(acc[i], scale, pair_of(base, i))
+                           : __fmul2_rn(acc[i], scale));
     }
-    store8<GT, LAY>(static_cast<GT*>(a.d_table) + at, col0, lane, a.dim, x);
+    store_raw8<GT, LAY>(static_cast<GT*>(a.d_table) + (int64_t)v * a.table_stride, col0, lane,
+                        a.dim, r);
   }
   // Parts are part_dim apart, a whole number of lanes: a lane finds its elements
   // where it left them, in either order of columns.
-  __device__ __forceinline__ void write_part(int64_t slot) {
+  __device__ __forceinline__ void write_part(int64_t slot) const {
     if (!within(slot, slot + 1, 0, 2 * a.blocks, a.err)) return;
-    store8<float, LAY>(a.parts + slot * a.part_dim, col0, lane, a.part_dim, acc);
-  }
-  __device__ __forceinline__ void add_part(int64_t slot) {
-    if (!within(slot, slot + 1, 0, 2 * a.blocks, a.err)) return;
-    const float* p = a.parts + slot * a.part_dim;
+    Raw8<float> r;
 #pragma unroll
-    for (int k = 0; k < kLane; ++k) {
-      const int c = column<LAY>(col0, lane, k);
-      if (c < a.part_dim) acc[k] = __fadd_rn(acc[k], __ldcg(p + c));
+    for (int i = 0; i < kLane / 2; ++i) set_pair(r, i, acc[i]);
+    store_raw8<float, LAY>(a.parts + slot * a.part_dim, col0, lane, a.part_dim, r);
+  }
+  // The parts of blocks from..to of one run, in their order.
+  __device__ __forceinline__ void add_parts(int64_t from, int64_t to) {
+    constexpr int kAtOnce = 4;
+    for (int64_t j0 = from; j0 <= to; j0 += kAtOnce) {
+      Raw8<float> r[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t j = j0 + u, slot = j == from ? 2 * j + 1 : 2 * j;
+        if (j <= to && within(slot, slot + 1, 0, 2 * a.blocks, a.err)) {
+          const float* p = a.parts + slot * a.part_dim;
+#pragma unroll
+          for (int k = 0; k < kLane; ++k) {
+            const int c = column<LAY>(col0, lane, k);
+            r[u].w[k] = __float_as_uint(c < a.part_dim ? __ldcg(p + c) : 0.0f);
+          }
+        } else {
+          r[u] = {};
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+        for (int i = 0; i < kLane / 2; ++i) acc[i] = __fadd2_rn(acc[i], pair_of(r[u], i));
     }
   }
 };
@@ -274,59 +356,116 @@ __device__ __forceinline__ int64_t lower_bound(const GradArgs& a, uint32_t v, in
   return lo;
 }
 
+// A warp to a block of sorted positions and a slab of columns. Its rows are asked
+// for kRows at a time whatever runs they belong to; a run's sum is written when
+// the next one starts.
 template <typename T, typename GT, Lay LAY>
 __global__ void __launch_bounds__(kThreads) sum_tokens_kernel(const __grid_constant__ GradArgs a) {
+  using R = Reduce<T, GT, LAY>;
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
   overlap_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t b = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
+  const int64_t b = item / a.slabs;
+  const int slab = (int)(item - b * a.slabs);
   if (b >= a.blocks) return;
   // keys and tokens of this block, of the two before and the two after it
-  const uint32_t none = 0xFFFFFFFFu;
-  auto key_at = [&](int64_t i) { return i >= 0 && i < a.rows ? a.keys[i] : none; };
+  auto key_at = [&](int64_t i) { return i >= 0 && i < a.rows ? a.keys[i] : kAll; };
   auto order_at = [&](int64_t i) { return i < a.rows ? a.order[i] : 0u; };
   const int64_t p = b * kBlock + lane;
-  const uint32_t before2 = key_at(p - 64), before = key_at(p - 32), here = key_at(p),
+  const uint32_t here = key_at(p), before = key_at(p - 32), before2 = key_at(p - 64),
                  after = key_at(p + 32), after2 = key_at(p + 64);
   const uint32_t order = order_at(p), order1 = order_at(p + 32), order2 = order_at(p + 64);
-  Reduce<T, GT, LAY> r{a, lane, (int)blockIdx.y * kSlab, {}};
-  for (int l = 0; l < kBlock;) {
-    const uint32_t v = __shfl_sync(none, here, l);
-    if (v >= (uint32_t)a.vocab) return;  // the tokens without a row, and the end
-    const int n = __popc(__ballot_sync(none, here == v));
-    const bool starts = l > 0 || __shfl_sync(none, before, 31) != v;
-    const int n_before =
-        starts ? 0
-               : __popc(__ballot_sync(none, before == v)) + __popc(__ballot_sync(none, before2 == v));
-    const int n1 = l + n < kBlock ? 0 : __popc(__ballot_sync(none, after == v));
-    const int n2 = n1 < 32 ? 0 : __popc(__ballot_sync(none, after2 == v));
+  const int n = __popc(__ballot_sync(kAll, here < (uint32_t)a.vocab));
+  if (n == 0) return;  // tokens without a row, and the end
+  // (the lanes' part of the warp's key before theirs)
+  const uint32_t last = __shfl_sync(kAll, before, 31);
+  const uint32_t left = __shfl_up_sync(kAll, here, 1);
+  const uint32_t starts = __ballot_sync(kAll, here != (lane == 0 ? last : left)) &
+                          (n == 32 ? kAll : (1u << n) - 1);
+  R r{a, lane, slab * kSlab, {}, {}};
+
+  // Joins the long run of v, whose part here was written: the last warp to get so
+  // far adds all parts.
+  auto join = [&](uint32_t v) {
+    const int64_t from = lower_bound(a, v, lane) / kBlock;
+    const int64_t to = (lower_bound(a, v + 1, lane) - 1) / kBlock;
+    __threadfence();
+    __syncwarp();
+    uint32_t done = 0;
+    if (lane == 0) done = atomicAdd(&a.tickets[slab * a.blocks + from], 1u);
+    done = __shfl_sync(kAll, done, 0);
+    if (done != (uint32_t)(to - from)) return;
+    __threadfence();
+    if (a.add) r.base = r.base_of(v);
     r.clear();
-    if (n_before + n + n1 + n2 <= kLongRun) {
-      if (starts) {
-        r.add_rows(order, l, n);
-        r.add_rows(order1, 0, n1);
-        r.add_rows(order2, 0, n2);
-        r.write(v);
+    r.add_parts(from, to);
+    r.write(v);
+  };
+
+  // Positions [0, begin) belong to a run that started before: part of a long one,
+  // or the business of the block where it started.
+  const int begin = starts ? __ffs(starts) - 1 : n;
+  if (begin > 0) {
+    const uint32_t v = __shfl_sync(kAll, here, 0);
+    const int n_before =
+        __popc(__ballot_sync(kAll, before == v)) + __popc(__ballot_sync(kAll, before2 == v));
+    const int n1 = begin < 32 ? 0 : __popc(__ballot_sync(kAll, after == v));
+    const int n2 = n1 < 32 ? 0 : __popc(__ballot_sync(kAll, after2 == v));
+    if (n_before + begin + n1 + n2 > kLongRun) {
+      r.clear();
+      for (int i0 = 0; i0 < begin; i0 += R::kRows) {
+        Raw8<T> rows[R::kRows];
+#pragma unroll
+        for (int u = 0; u < R::kRows; ++u)
+          if (i0 + u < begin) rows[u] = r.row(__shfl_sync(kAll, order, i0 + u));
+#pragma unroll
+        for (int u = 0; u < R::kRows; ++u)
+          if (i0 + u < begin) r.add(rows[u]);
       }
-    } else {
-      // This block's part: place 2b + 1 if the run starts here, else 2b.
-      r.add_rows(order, l, n);
-      r.write_part(2 * b + starts);
-      const int64_t from = lower_bound(a, v, lane) / kBlock;
-      const int64_t to = (lower_bound(a, v + 1, lane) - 1) / kBlock;
-      __threadfence();
-      __syncwarp();
-      uint32_t done = 0;
-      if (lane == 0) done = atomicAdd(&a.tickets[blockIdx.y * a.blocks + from], 1u);
-      done = __shfl_sync(none, done, 0);
-      if (done == (uint32_t)(to - from)) {
-        __threadfence();
-        r.clear();
-        r.add_part(2 * from + 1);
-        for (int64_t j = from + 1; j <= to; ++j) r.add_part(2 * j);
-        r.write(v);
-      }
+      r.write_part(2 * b);
+      join(v);
     }
-    l += n;
+  }
+  if (!starts) return;
+
+  // The runs that start here; the last one may go on behind this block.
+  const int s_last = 31 - __clz(starts);
+  const uint32_t v_last = __shfl_sync(kAll, here, s_last);
+  const int n1 = n < 32 ? 0 : __popc(__ballot_sync(kAll, after == v_last));
+  const int n2 = n1 < 32 ? 0 : __popc(__ballot_sync(kAll, after2 == v_last));
+  const bool is_long = n - s_last + n1 + n2 > kLongRun;
+  const int end = is_long ? n : n + n1 + n2;
+  uint32_t v = 0;
+  for (int i0 = begin; i0 < end; i0 += R::kRows) {
+    Raw8<T> rows[R::kRows];
+    Raw8<GT> bases[R::kRows];
+#pragma unroll
+    for (int u = 0; u < R::kRows; ++u) {
+      const int i = i0 + u;
+      if (i >= end) break;
+      rows[u] = r.row(__shfl_sync(kAll, i < 32 ? order : i < 64 ? order1 : order2, i & 31));
+      if (a.add && i < 32 && (starts >> i & 1))
+        bases[u] = r.base_of(__shfl_sync(kAll, here, i));
+    }
+#pragma unroll
+    for (int u = 0; u < R::kRows; ++u) {
+      const int i = i0 + u;
+      if (i >= end) break;
+      if (i < 32 && (starts >> i & 1)) {
+        if (i > begin) r.write(v);
+        v = __shfl_sync(kAll, here, i);
+        r.clear();
+        if (a.add) r.base = bases[u];
+      }
+      r.add(rows[u]);
+    }
+  }
+  if (is_long) {
+    r.write_part(2 * b + 1);
+    join(v_last);
+  } else {
+    r.write(v);
   }
 }
 
@@ -339,14 +478,30 @@ cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
 }
 
 template <typename T, typename GT, Lay LAY>
-cudaError_t launch_sums(const GradArgs& a, bool fill, bool sums, cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  if (fill)
-    e = launch_kernel(fill_rows_kernel<GT, LAY>, dim3((unsigned)((a.vocab + kWarps - 1) / kWarps)),
-                      dim3(kThreads), 0, stream, a);
-  if (e != cudaSuccess || !sums) return e;
-  const dim3 grid((unsigned)((a.blocks + kWarps - 1) / kWarps), (unsigned)a.slabs);
-  return launch_kernel(sum_tokens_kernel<T, GT, LAY>, grid, dim3(kThreads), 0, stream, a);
+cudaError_t launch_sums(const SortArgs& k, const GradArgs& a, cudaStream_t stream) {
+  const bool fill = a.add != a.d_table;
+  if (k.rows > 0 || fill) {
+    const int smem = (int)sizeof(SortShared) + (kSortWarps * (int)sizeof(uint32_t) << k.bits);
+    auto* kernel = sort_and_fill_kernel<GT, LAY>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(SortShared) +
+                                             kSortWarps * kMaxDigits * (int)sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
+    // Fill blocks: whole clusters, at most four times as many as fit the SMs, so that
+    // the last ones to start are a small part of the work.
+    const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT);
+    const int64_t clusters = (bytes + kSortBlocks * kFillBytes - 1) / (kSortBlocks * kFillBytes);
+    const int64_t most = 4 * 152 / kSortBlocks;
+    const int64_t grid = (k.rows > 0 ? kSortBlocks : 0) +
+                         (fill ? kSortBlocks * (clusters < most ? clusters : most) : 0);
+    e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kSortThreads), smem, stream, k, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (k.rows == 0) return cudaSuccess;
+  const int64_t warps = a.blocks * a.slabs;
+  return launch_kernel(sum_tokens_kernel<T, GT, LAY>,
+                       dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, stream,
+                       a);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -418,51 +573,45 @@ cudaError_t launch_embedding_grad(const EmbeddingLaunch& in, cudaStream_t stream
   a.scale = (float)in.scale;
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
+  SortArgs k = {};
+  k.rows = in.rows;
+  k.bits = 1;
   if (in.rows > 0) {
-    a.keys = reinterpret_cast<uint32_t*>(ws + s.keys);
-    a.order = reinterpret_cast<uint32_t*>(ws + s.order);
-    a.tickets = reinterpret_cast<uint32_t*>(ws + s.tickets);
-    a.parts = reinterpret_cast<float*>(ws + s.parts);
-    SortArgs k;
     k.tokens = in.tokens;
     k.keys = reinterpret_cast<uint32_t*>(ws + s.keys);
     k.order = reinterpret_cast<uint32_t*>(ws + s.order);
     k.keys2 = reinterpret_cast<uint32_t*>(ws + s.keys2);
     k.order2 = reinterpret_cast<uint32_t*>(ws + s.order2);
-    k.tickets = a.tickets;
-    k.rows = in.rows;
+    k.tickets = reinterpret_cast<uint32_t*>(ws + s.tickets);
     k.n_tickets = s.n_tickets;
+    constexpr int64_t kAllWarps = kSortBlocks * kSortWarps;
+    k.share = ((in.rows + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;
     k.vocab = a.vocab;
     int bits = 1;
     while (in.vocab >> bits) ++bits;  // keys 0..vocab
     k.passes = (bits + 9) / 10;
     k.bits = (bits + k.passes - 1) / k.passes;
-    k.err = a.err;
-    const int smem = kSortWarps * (int)sizeof(uint32_t) << k.bits;
-    cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortWarps * kMaxDigits * (int)sizeof(uint32_t));
-    if (e == cudaSuccess)
-      e = launch_kernel(sort_tokens_kernel, dim3(1), dim3(kSortThreads), smem, stream, k);
-    if (e != cudaSuccess) return e;
+    a.keys = k.keys;
+    a.order = k.order;
+    a.tickets = k.tickets;
+    a.parts = reinterpret_cast<float*>(ws + s.parts);
   }
   const bool br = in.dtype == ZS_BF16, bt = in.table_dtype == ZS_BF16;
   const bool vec = rows_aligned(a.d_out, a.row_stride, br ? 2 : 4) &&
                    rows_aligned(a.d_table, a.table_stride, bt ? 2 : 4) &&
                    rows_aligned(a.add, a.table_stride, bt ? 2 : 4);
-  const bool fill = a.add != a.d_table, sums = in.rows > 0;
   if (br) {
     if (bt)
-      return vec ? launch_sums<__nv_bfloat16, __nv_bfloat16, kEight>(a, fill, sums, stream)
-                 : launch_sums<__nv_bfloat16, __nv_bfloat16, kOne>(a, fill, sums, stream);
-    return vec ? launch_sums<__nv_bfloat16, float, kEight>(a, fill, sums, stream)
-               : launch_sums<__nv_bfloat16, float, kOne>(a, fill, sums, stream);
+      return vec ? launch_sums<__nv_bfloat16, __nv_bfloat16, kEight>(k, a, stream)
+                 : launch_sums<__nv_bfloat16, __nv_bfloat16, kOne>(k, a, stream);
+    return vec ? launch_sums<__nv_bfloat16, float, kEight>(k, a, stream)
+               : launch_sums<__nv_bfloat16, float, kOne>(k, a, stream);
   }
   if (bt)
-    return vec ? launch_sums<float, __nv_bfloat16, kEight>(a, fill, sums, stream)
-               : launch_sums<float, __nv_bfloat16, kOne>(a, fill, sums, stream);
-  return vec ? launch_sums<float, float, kEight>(a, fill, sums, stream)
-             : launch_sums<float, float, kOne>(a, fill, sums, stream);
+    return vec ? launch_sums<float, __nv_bfloat16, kEight>(k, a, stream)
+               : launch_sums<float, __nv_bfloat16, kOne>(k, a, stream);
+  return vec ? launch_sums<float, float, kEight>(k, a, stream)
+             : launch_sums<float, float, kOne>(k, a, stream);
 }
 
 }  // namespace zs
