@@ -6,14 +6,16 @@
 //
 // The gradient sorts the tokens (a stable counting sort, so that a row's sum
 // runs over its tokens in their order) and then takes the sorted positions in
-// blocks of 32, a warp to a block and a slab of 256 columns. A run of up to 64
-// equal tokens is summed by the warp in whose block it starts; of a longer one
-// each block's part goes to scratch memory, and the warp that finishes last adds
-// the parts in their order. So the work of a warp is bounded however often a
-// token occurs, each table row is written once, and no sum depends on timing.
+// blocks of 256, 32 a warp, for a slab of 256 columns. A run of equal tokens
+// within a warp's 32 is summed by it; the parts of longer ones and of those that
+// cross warps are added in their order, through shared memory and, across blocks,
+// scratch memory. So the work of a warp is bounded however often a token occurs,
+// and no sum depends on timing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "bounds.cuh"
 #include "overlap.cuh"
@@ -221,16 +223,25 @@ template <typename GT, Lay LAY>
 __device__ void fill_rows(const GradArgs& a, int64_t block, int64_t blocks) {
   const int lane = threadIdx.x & 31;
   if (LAY != kOne && a.table_stride == a.dim && ((uintptr_t)a.d_table | (uintptr_t)a.add) % 32 == 0) {
-    // dense: 32 bytes a thread
+    // dense: 32 bytes a thread, four times over
     const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT), whole = bytes / 32 * 32;
     unsigned char* to = static_cast<unsigned char*>(a.d_table);
     const unsigned char* from = static_cast<const unsigned char*>(a.add);
-    for (int64_t i = block * kFillBytes + threadIdx.x * 32; i < whole;
-         i += blocks * kFillBytes) {
-      if (!within(i, i + 32, 0, bytes, a.err)) continue;
-      uint32_t w[8] = {};
-      if (from) load_words<8>(w, from + i);
-      store_words<8>(to + i, w);
+    constexpr int kAtOnce = 4;
+    for (int64_t i0 = block * kAtOnce * kFillBytes + threadIdx.x * 32; i0 < whole;
+         i0 += blocks * kAtOnce * kFillBytes) {
+      uint32_t w[kAtOnce][8] = {};
+      if (from)
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int64_t i = i0 + u * kFillBytes;
+          if (i < whole && within(i, i + 32, 0, bytes, a.err)) load_words<8>(w[u], from + i);
+        }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int64_t i = i0 + u * kFillBytes;
+        if (i < whole && within(i, i + 32, 0, bytes, a.err)) store_words<8>(to + i, w[u]);
+      }
     }
     for (int64_t i = whole + threadIdx.x * (int)sizeof(GT); block == 0 && i < bytes;
          i += kSortThreads * (int)sizeof(GT)) {
@@ -266,12 +277,26 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks,
 }
 
 // ---- sums over sorted tokens -----------------------------------------------------
-constexpr int kBlock = 32;    // sorted positions of a warp
-constexpr int kLongRun = 64;  // equal tokens that one warp sums by itself
+constexpr int kBlock = 32 * kWarps;  // sorted positions of a block, 32 a warp
 
-template <typename T, typename GT, Lay LAY>
+// What a warp of a block knows of its first and its last run.
+struct Edges {
+  uint32_t v_first, v_last;
+  bool from_before, to_next;  // the first began before this warp, the last goes on behind it
+  bool one;                   // they are one run (and its part is that of the first)
+};
+// The parts of runs that cross warps: of the first run, if it began before, and of
+// the last, if it goes on.
+struct Crossing {
+  Edges edges[kWarps];
+  float2 parts[kWarps][2][kLane / 2][32];
+};
+
+// ADD: the sums are added to something.
+template <typename T, typename GT, Lay LAY, bool ADD>
 struct Reduce {
-  static constexpr int kRows = 16 / (int)sizeof(T);  // on their way at once
+  static constexpr int kWords = kLane / 4 * ((int)sizeof(T) + (ADD ? (int)sizeof(GT) : 0));
+  static constexpr int kRows = kWords <= 4 ? 16 : 8;  // on their way at once
   const GradArgs& a;
   const int lane, col0;
   float2 acc[kLane / 2];
@@ -301,14 +326,22 @@ struct Reduce {
 #pragma unroll
     for (int i = 0; i < kLane / 2; ++i) {
       const float2 scale = {a.scale, a.scale};
-      set_pair(r, i, a.add ? __ffma2_rn(acc[i], scale, pair_of(base, i))
-                           : __fmul2_rn(acc[i], scale));
+      set_pair(r, i, ADD ? __ffma2_rn(acc[i], scale, pair_of(base, i))
+                         : __fmul2_rn(acc[i], scale));
     }
     store_raw8<GT, LAY>(static_cast<GT*>(a.d_table) + (int64_t)v * a.table_stride, col0, lane,
                         a.dim, r);
   }
-  // Parts are part_dim apart, a whole number of lanes: a lane finds its elements
-  // where it left them, in either order of columns.
+  __device__ __forceinline__ void keep(float2 (*part)[32]) const {
+#pragma unroll
+    for (int i = 0; i < kLane / 2; ++i) part[i][lane] = acc[i];
+  }
+  __device__ __forceinline__ void add_kept(const float2 (*part)[32]) {
+#pragma unroll
+    for (int i = 0; i < kLane / 2; ++i) acc[i] = __fadd2_rn(acc[i], part[i][lane]);
+  }
+  // Parts in scratch memory are part_dim apart, a whole number of lanes: a lane
+  // finds its elements where it left them, in either order of columns.
   __device__ __forceinline__ void write_part(int64_t slot) const {
     if (!within(slot, slot + 1, 0, 2 * a.blocks, a.err)) return;
     Raw8<float> r;
@@ -318,21 +351,20 @@ struct Reduce {
   }
   // The parts of blocks from..to of one run, in their order.
   __device__ __forceinline__ void add_parts(int64_t from, int64_t to) {
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 8;
     for (int64_t j0 = from; j0 <= to; j0 += kAtOnce) {
       Raw8<float> r[kAtOnce];
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const int64_t j = j0 + u, slot = j == from ? 2 * j + 1 : 2 * j;
+        r[u] = {};
         if (j <= to && within(slot, slot + 1, 0, 2 * a.blocks, a.err)) {
           const float* p = a.parts + slot * a.part_dim;
 #pragma unroll
           for (int k = 0; k < kLane; ++k) {
             const int c = column<LAY>(col0, lane, k);
-            r[u].w[k] = __float_as_uint(c < a.part_dim ? __ldcg(p + c) : 0.0f);
+            if (c < a.part_dim) r[u].w[k] = __float_as_uint(__ldcg(p + c));
           }
-        } else {
-          r[u] = {};
         }
       }
 #pragma unroll
@@ -343,129 +375,151 @@ struct Reduce {
   }
 };
 
-// The first sorted position whose key is at least v (32 probes a step).
-__device__ __forceinline__ int64_t lower_bound(const GradArgs& a, uint32_t v, int lane) {
-  int64_t lo = 0, hi = a.rows;  // keys before lo are below v, from hi on they are not
-  while (lo < hi) {
-    const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < hi && a.keys[at] < v);
-    const int n = __popc(below);
-    if (n < 32 && lo + n * step < hi) hi = lo + n * step;
-    if (n > 0) lo += (n - 1) * step + 1;
+// The first sorted positions whose keys are at least v and v + 1 (32 probes a step,
+// both searches' on their way together).
+__device__ __forceinline__ void run_of(const GradArgs& a, uint32_t v, int lane, int64_t* from,
+                                       int64_t* to) {
+  int64_t lo[2] = {0, 0}, hi[2] = {a.rows, a.rows};  // keys before lo are below, from hi on not
+  while (lo[0] < hi[0] || lo[1] < hi[1]) {
+    int64_t step[2];
+    bool below[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      step[k] = (hi[k] - lo[k] + 31) / 32;
+      const int64_t at = lo[k] + lane * step[k];
+      below[k] = at < hi[k] && __ldcg(a.keys + at) < v + k;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, below[k]));
+      if (lo[k] >= hi[k]) continue;
+      if (n < 32 && lo[k] + n * step[k] < hi[k]) hi[k] = lo[k] + n * step[k];
+      if (n > 0) lo[k] += (n - 1) * step[k] + 1;
+    }
   }
-  return lo;
+  *from = lo[0];
+  *to = lo[1];
 }
 
-// A warp to a block of sorted positions and a slab of columns. Its rows are asked
-// for kRows at a time whatever runs they belong to; a run's sum is written when
-// the next one starts.
-template <typename T, typename GT, Lay LAY>
-__global__ void __launch_bounds__(kThreads) sum_tokens_kernel(const __grid_constant__ GradArgs a) {
-  using R = Reduce<T, GT, LAY>;
+// A block to kBlock sorted positions and a slab of columns. A warp's rows are asked
+// for kRows at a time whatever runs they belong to; a run's sum is written when the
+// next one starts. Runs that cross warps are put together in shared memory by the
+// warp in which they start, those that cross blocks from scratch memory by the
+// block that is through with its part last.
+template <typename T, typename GT, Lay LAY, bool ADD>
+__global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_constant__ GradArgs a) {
+  using R = Reduce<T, GT, LAY, ADD>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
+  __shared__ Crossing sh;
   overlap_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  const int64_t b = item / a.slabs;
-  const int slab = (int)(item - b * a.slabs);
-  if (b >= a.blocks) return;
-  // keys and tokens of this block, of the two before and the two after it
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int64_t b = blockIdx.x / a.slabs;
+  const int slab = (int)(blockIdx.x - b * a.slabs);
+  const int64_t p0 = b * kBlock + warp * 32, p = p0 + lane;
   auto key_at = [&](int64_t i) { return i >= 0 && i < a.rows ? a.keys[i] : kAll; };
-  auto order_at = [&](int64_t i) { return i < a.rows ? a.order[i] : 0u; };
-  const int64_t p = b * kBlock + lane;
-  const uint32_t here = key_at(p), before = key_at(p - 32), before2 = key_at(p - 64),
-                 after = key_at(p + 32), after2 = key_at(p + 64);
-  const uint32_t order = order_at(p), order1 = order_at(p + 32), order2 = order_at(p + 64);
-  const int n = __popc(__ballot_sync(kAll, here < (uint32_t)a.vocab));
-  if (n == 0) return;  // tokens without a row, and the end
-  // (the lanes' part of the warp's key before theirs)
-  const uint32_t last = __shfl_sync(kAll, before, 31);
+  const uint32_t here = key_at(p), beside = key_at(lane == 0 ? p0 - 1 : p0 + 32);
+  const uint32_t order = p < a.rows ? a.order[p] : 0;
+  const int n = __popc(__ballot_sync(kAll, here < (uint32_t)a.vocab));  // (the rest has no row)
+  const uint32_t before = __shfl_sync(kAll, beside, 0), next = __shfl_sync(kAll, beside, 31);
   const uint32_t left = __shfl_up_sync(kAll, here, 1);
-  const uint32_t starts = __ballot_sync(kAll, here != (lane == 0 ? last : left)) &
+  const uint32_t starts = __ballot_sync(kAll, here != (lane == 0 ? before : left)) &
                           (n == 32 ? kAll : (1u << n) - 1);
   R r{a, lane, slab * kSlab, {}, {}};
-
-  // Joins the long run of v, whose part here was written: the last warp to get so
-  // far adds all parts.
-  auto join = [&](uint32_t v) {
-    const int64_t from = lower_bound(a, v, lane) / kBlock;
-    const int64_t to = (lower_bound(a, v + 1, lane) - 1) / kBlock;
-    __threadfence();
-    __syncwarp();
-    uint32_t done = 0;
-    if (lane == 0) done = atomicAdd(&a.tickets[slab * a.blocks + from], 1u);
-    done = __shfl_sync(kAll, done, 0);
-    if (done != (uint32_t)(to - from)) return;
-    __threadfence();
-    if (a.add) r.base = r.base_of(v);
-    r.clear();
-    r.add_parts(from, to);
-    r.write(v);
-  };
-
-  // Positions [0, begin) belong to a run that started before: part of a long one,
-  // or the business of the block where it started.
-  const int begin = starts ? __ffs(starts) - 1 : n;
-  if (begin > 0) {
-    const uint32_t v = __shfl_sync(kAll, here, 0);
-    const int n_before =
-        __popc(__ballot_sync(kAll, before == v)) + __popc(__ballot_sync(kAll, before2 == v));
-    const int n1 = begin < 32 ? 0 : __popc(__ballot_sync(kAll, after == v));
-    const int n2 = n1 < 32 ? 0 : __popc(__ballot_sync(kAll, after2 == v));
-    if (n_before + begin + n1 + n2 > kLongRun) {
-      r.clear();
-      for (int i0 = 0; i0 < begin; i0 += R::kRows) {
-        Raw8<T> rows[R::kRows];
-#pragma unroll
-        for (int u = 0; u < R::kRows; ++u)
-          if (i0 + u < begin) rows[u] = r.row(__shfl_sync(kAll, order, i0 + u));
-#pragma unroll
-        for (int u = 0; u < R::kRows; ++u)
-          if (i0 + u < begin) r.add(rows[u]);
-      }
-      r.write_part(2 * b);
-      join(v);
-    }
+  Edges e = {};
+  if (n > 0) {
+    e.v_first = __shfl_sync(kAll, here, 0);
+    e.v_last = __shfl_sync(kAll, here, n - 1);
+    e.from_before = !(starts & 1);
+    e.to_next = n == 32 && next == e.v_last;
+    e.one = starts == 0;
   }
-  if (!starts) return;
-
-  // The runs that start here; the last one may go on behind this block.
-  const int s_last = 31 - __clz(starts);
-  const uint32_t v_last = __shfl_sync(kAll, here, s_last);
-  const int n1 = n < 32 ? 0 : __popc(__ballot_sync(kAll, after == v_last));
-  const int n2 = n1 < 32 ? 0 : __popc(__ballot_sync(kAll, after2 == v_last));
-  const bool is_long = n - s_last + n1 + n2 > kLongRun;
-  const int end = is_long ? n : n + n1 + n2;
-  uint32_t v = 0;
-  for (int i0 = begin; i0 < end; i0 += R::kRows) {
+  if (lane == 0) sh.edges[warp] = e;
+  uint32_t v = e.v_first;
+  bool before_me = e.from_before;  // of the run at work
+  r.clear();
+  for (int i0 = 0; i0 < n; i0 += R::kRows) {
     Raw8<T> rows[R::kRows];
-    Raw8<GT> bases[R::kRows];
+    Raw8<GT> bases[ADD ? R::kRows : 1];
 #pragma unroll
     for (int u = 0; u < R::kRows; ++u) {
       const int i = i0 + u;
-      if (i >= end) break;
-      rows[u] = r.row(__shfl_sync(kAll, i < 32 ? order : i < 64 ? order1 : order2, i & 31));
-      if (a.add && i < 32 && (starts >> i & 1))
-        bases[u] = r.base_of(__shfl_sync(kAll, here, i));
+      if (i >= n) break;
+      rows[u] = r.row(__shfl_sync(kAll, order, i));
+      if (ADD && (starts >> i & 1)) bases[ADD ? u : 0] = r.base_of(__shfl_sync(kAll, here, i));
     }
 #pragma unroll
     for (int u = 0; u < R::kRows; ++u) {
       const int i = i0 + u;
-      if (i >= end) break;
-      if (i < 32 && (starts >> i & 1)) {
-        if (i > begin) r.write(v);
+      if (i >= n) break;
+      if (starts >> i & 1) {
+        if (i > 0) {
+          if (before_me)
+            r.keep(sh.parts[warp][0]);
+          else
+            r.write(v);
+        }
         v = __shfl_sync(kAll, here, i);
+        before_me = false;
         r.clear();
-        if (a.add) r.base = bases[u];
+        if (ADD) r.base = bases[ADD ? u : 0];
       }
       r.add(rows[u]);
     }
   }
-  if (is_long) {
-    r.write_part(2 * b + 1);
-    join(v_last);
-  } else {
+  if (n > 0) {
+    if (before_me)
+      r.keep(sh.parts[warp][0]);
+    else if (e.to_next)
+      r.keep(sh.parts[warp][1]);
+    else
+      r.write(v);
+  }
+  __syncthreads();
+
+  // Adds the parts of a run from warp w on; whether it ends within the block.
+  auto add_from = [&](int w) {
+    for (; w < kWarps; ++w) {
+      r.add_kept(sh.parts[w][0]);
+      if (!sh.edges[w].one || !sh.edges[w].to_next) return true;
+    }
+    return false;
+  };
+  // Joins the run of v, whose part of this block was written.
+  auto join = [&](uint32_t v) {
+    int64_t from, to;
+    run_of(a, v, lane, &from, &to);
+    from /= kBlock;
+    to = (to - 1) / kBlock;
+    __threadfence();
+    __syncwarp();
+    uint32_t done = 0;
+    if (lane == 0 && within(from, from + 1, 0, a.blocks, a.err))
+      done = atomicAdd(&a.tickets[slab * a.blocks + from], 1u);
+    done = __shfl_sync(kAll, done, 0);
+    if (done != (uint32_t)(to - from)) return;
+    __threadfence();
+    if (ADD) r.base = r.base_of(v);
+    r.clear();
+    r.add_parts(from, to);
     r.write(v);
+  };
+  if (n == 0) return;
+  if (warp == 0 && e.from_before) {  // began in a block before
+    r.clear();
+    add_from(0);
+    r.write_part(2 * b);
+    join(e.v_first);
+  }
+  if (e.to_next && !(e.one && e.from_before)) {  // starts in this warp
+    r.clear();
+    r.add_kept(sh.parts[warp][1]);
+    if (add_from(warp + 1)) {
+      if (ADD) r.base = r.base_of(e.v_last);
+      r.write(e.v_last);
+    } else {
+      r.write_part(2 * b + 1);
+      join(e.v_last);
+    }
   }
 }
 
@@ -477,31 +531,59 @@ cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
              : launch_kernel(embedding_kernel<TT, OT, kOne>, grid, dim3(kThreads), 0, stream, a);
 }
 
+constexpr int kSortSmem =
+    (int)sizeof(SortShared) + kSortWarps * kMaxDigits * (int)sizeof(uint32_t);
+
+// How many clusters of the sorting kernel the current device runs at the same time
+// (asked once: every variant has the same threads and shared memory).
+cudaError_t clusters_at_once(const void* kernel, int* n) {
+  static std::atomic<int> of_device[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool listed = dev >= 0 && dev < 64;
+  *n = listed ? of_device[dev].load(std::memory_order_relaxed) : 0;
+  if (*n > 0) return cudaSuccess;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kSortBlocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSortBlocks);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = kSortSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  if (e == cudaSuccess && listed) of_device[dev].store(*n, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename T, typename GT, Lay LAY>
 cudaError_t launch_sums(const SortArgs& k, const GradArgs& a, cudaStream_t stream) {
   const bool fill = a.add != a.d_table;
   if (k.rows > 0 || fill) {
-    const int smem = (int)sizeof(SortShared) + (kSortWarps * (int)sizeof(uint32_t) << k.bits);
     auto* kernel = sort_and_fill_kernel<GT, LAY>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(SortShared) +
-                                             kSortWarps * kMaxDigits * (int)sizeof(uint32_t));
+                                         kSortSmem);
     if (e != cudaSuccess) return e;
-    // Fill blocks: whole clusters, at most four times as many as fit the SMs, so that
-    // the last ones to start are a small part of the work.
+    // Fill blocks: as many clusters as run at the same time, the sorting one taken off.
+    int fit = 0;
+    e = clusters_at_once((const void*)kernel, &fit);
+    if (e != cudaSuccess) return e;
     const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT);
     const int64_t clusters = (bytes + kSortBlocks * kFillBytes - 1) / (kSortBlocks * kFillBytes);
-    const int64_t most = 4 * 152 / kSortBlocks;
+    const int64_t most = fit > 1 ? fit - 1 : 1;
     const int64_t grid = (k.rows > 0 ? kSortBlocks : 0) +
                          (fill ? kSortBlocks * (clusters < most ? clusters : most) : 0);
-    e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kSortThreads), smem, stream, k, a);
+    e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kSortThreads), kSortSmem, stream, k,
+                      a);
     if (e != cudaSuccess) return e;
   }
   if (k.rows == 0) return cudaSuccess;
-  const int64_t warps = a.blocks * a.slabs;
-  return launch_kernel(sum_tokens_kernel<T, GT, LAY>,
-                       dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kThreads), 0, stream,
-                       a);
+  return launch_kernel(a.add ? sum_tokens_kernel<T, GT, LAY, true>
+                             : sum_tokens_kernel<T, GT, LAY, false>,
+                       dim3((unsigned)(a.blocks * a.slabs)), dim3(kThreads), 0, stream, a);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
