@@ -6,8 +6,8 @@
 //
 // The gradient sorts the tokens (a stable counting sort, so that a row's sum
 // runs over its tokens in their order) and then takes the sorted positions in
-// blocks of 256, 32 a warp, for a slab of 256 columns. A run of equal tokens
-// within a warp's 32 is summed by it; the parts of longer ones and of those that
+// blocks of 256, 16 a warp, for a slab of 256 columns. A run of equal tokens
+// within a warp's 16 is summed by it; the parts of longer ones and of those that
 // cross warps are added in their order, through shared memory and, across blocks,
 // scratch memory. So the work of a warp is bounded however often a token occurs,
 // and no sum depends on timing.
@@ -277,7 +277,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks,
 }
 
 // ---- sums over sorted tokens -----------------------------------------------------
-constexpr int kBlock = 32 * kWarps;  // sorted positions of a block, 32 a warp
+constexpr int kSumThreads = 512;
+constexpr int kSumWarps = kSumThreads / 32;
+constexpr int kEach = 16;                   // sorted positions of a warp
+constexpr int kBlock = kEach * kSumWarps;  // and of a block
 
 // What a warp of a block knows of its first and its last run.
 struct Edges {
@@ -288,8 +291,9 @@ struct Edges {
 // The parts of runs that cross warps: of the first run, if it began before, and of
 // the last, if it goes on.
 struct Crossing {
-  Edges edges[kWarps];
-  float2 parts[kWarps][2][kLane / 2][32];
+  Edges edges[kSumWarps];
+  int64_t from[2], to[2];  // of the block's first run and its last, where they cross blocks
+  float2 parts[kSumWarps][2][kLane / 2][32];
 };
 
 // ADD: the sums are added to something.
@@ -407,37 +411,41 @@ __device__ __forceinline__ void run_of(const GradArgs& a, uint32_t v, int lane, 
 // warp in which they start, those that cross blocks from scratch memory by the
 // block that is through with its part last.
 template <typename T, typename GT, Lay LAY, bool ADD>
-__global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(kSumThreads, 1)
+    sum_tokens_kernel(const __grid_constant__ GradArgs a) {
   using R = Reduce<T, GT, LAY, ADD>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  __shared__ Crossing sh;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Crossing& sh = *reinterpret_cast<Crossing*>(smem);
   overlap_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t b = blockIdx.x / a.slabs;
   const int slab = (int)(blockIdx.x - b * a.slabs);
-  const int64_t p0 = b * kBlock + warp * 32, p = p0 + lane;
-  auto key_at = [&](int64_t i) { return i >= 0 && i < a.rows ? a.keys[i] : kAll; };
-  const uint32_t here = key_at(p), beside = key_at(lane == 0 ? p0 - 1 : p0 + 32);
-  const uint32_t order = p < a.rows ? a.order[p] : 0;
-  const int n = __popc(__ballot_sync(kAll, here < (uint32_t)a.vocab));  // (the rest has no row)
-  const uint32_t before = __shfl_sync(kAll, beside, 0), next = __shfl_sync(kAll, beside, 31);
-  const uint32_t left = __shfl_up_sync(kAll, here, 1);
-  const uint32_t starts = __ballot_sync(kAll, here != (lane == 0 ? before : left)) &
-                          (n == 32 ? kAll : (1u << n) - 1);
+  const int64_t p0 = b * kBlock + warp * kEach;
+  // the warp's keys, and one to either side
+  const int64_t p = lane == 31 ? p0 - 1 : p0 + lane;
+  const uint32_t here = p >= 0 && p < a.rows ? a.keys[p] : kAll;
+  const uint32_t order = lane < kEach && p < a.rows ? a.order[p] : 0;
+  const uint32_t left = __shfl_sync(kAll, here, (lane + 31) & 31);
+  const uint32_t next = __shfl_sync(kAll, here, kEach);
+  // tokens with a row, and the first ones of their runs
+  const int n = __popc(__ballot_sync(kAll, lane < kEach && here < (uint32_t)a.vocab));
+  const uint32_t starts = __ballot_sync(kAll, lane < n && here != left);
   R r{a, lane, slab * kSlab, {}, {}};
   Edges e = {};
   if (n > 0) {
     e.v_first = __shfl_sync(kAll, here, 0);
     e.v_last = __shfl_sync(kAll, here, n - 1);
     e.from_before = !(starts & 1);
-    e.to_next = n == 32 && next == e.v_last;
+    e.to_next = n == kEach && next == e.v_last;
     e.one = starts == 0;
   }
   if (lane == 0) sh.edges[warp] = e;
   uint32_t v = e.v_first;
   bool before_me = e.from_before;  // of the run at work
   r.clear();
-  for (int i0 = 0; i0 < n; i0 += R::kRows) {
+#pragma unroll
+  for (int i0 = 0; i0 < kEach; i0 += R::kRows) {
     Raw8<T> rows[R::kRows];
     Raw8<GT> bases[ADD ? R::kRows : 1];
 #pragma unroll
@@ -446,6 +454,16 @@ __global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_co
       if (i >= n) break;
       rows[u] = r.row(__shfl_sync(kAll, order, i));
       if (ADD && (starts >> i & 1)) bases[ADD ? u : 0] = r.base_of(__shfl_sync(kAll, here, i));
+    }
+    // while they are on their way: how far the runs that cross the block's ends go
+    if (i0 == 0 && ((warp == 0 && e.from_before) || (warp == kSumWarps - 1 && e.to_next))) {
+      const int end = warp == 0 && e.from_before ? 0 : 1;
+      int64_t from, to;
+      run_of(a, end ? e.v_last : e.v_first, lane, &from, &to);
+      if (lane == 0) {
+        sh.from[end] = from / kBlock;
+        sh.to[end] = (to - 1) / kBlock;
+      }
     }
 #pragma unroll
     for (int u = 0; u < R::kRows; ++u) {
@@ -475,21 +493,19 @@ __global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_co
       r.write(v);
   }
   __syncthreads();
+  if (n == 0) return;
 
   // Adds the parts of a run from warp w on; whether it ends within the block.
   auto add_from = [&](int w) {
-    for (; w < kWarps; ++w) {
+    for (; w < kSumWarps; ++w) {
       r.add_kept(sh.parts[w][0]);
       if (!sh.edges[w].one || !sh.edges[w].to_next) return true;
     }
     return false;
   };
   // Joins the run of v, whose part of this block was written.
-  auto join = [&](uint32_t v) {
-    int64_t from, to;
-    run_of(a, v, lane, &from, &to);
-    from /= kBlock;
-    to = (to - 1) / kBlock;
+  auto join = [&](uint32_t v, int end) {
+    const int64_t from = sh.from[end], to = sh.to[end];
     __threadfence();
     __syncwarp();
     uint32_t done = 0;
@@ -503,12 +519,11 @@ __global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_co
     r.add_parts(from, to);
     r.write(v);
   };
-  if (n == 0) return;
   if (warp == 0 && e.from_before) {  // began in a block before
     r.clear();
     add_from(0);
     r.write_part(2 * b);
-    join(e.v_first);
+    join(e.v_first, 0);
   }
   if (e.to_next && !(e.one && e.from_before)) {  // starts in this warp
     r.clear();
@@ -518,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 2) sum_tokens_kernel(const __grid_co
       r.write(e.v_last);
     } else {
       r.write_part(2 * b + 1);
-      join(e.v_last);
+      join(e.v_last, 1);
     }
   }
 }
@@ -581,9 +596,13 @@ cudaError_t launch_sums(const SortArgs& k, const GradArgs& a, cudaStream_t strea
     if (e != cudaSuccess) return e;
   }
   if (k.rows == 0) return cudaSuccess;
-  return launch_kernel(a.add ? sum_tokens_kernel<T, GT, LAY, true>
-                             : sum_tokens_kernel<T, GT, LAY, false>,
-                       dim3((unsigned)(a.blocks * a.slabs)), dim3(kThreads), 0, stream, a);
+  auto* kernel =
+      a.add ? sum_tokens_kernel<T, GT, LAY, true> : sum_tokens_kernel<T, GT, LAY, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)sizeof(Crossing));
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3((unsigned)(a.blocks * a.slabs)), dim3(kSumThreads),
+                       sizeof(Crossing), stream, a);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }

@@ -614,7 +614,7 @@ zs_status zs_embedding(const void* table, zs_dtype table_dtype, int64_t vocab, i
 int64_t zs_embedding_grad_workspace_bytes(int64_t rows, int64_t dim);
 /* zs_embedding_grad — the table's gradient:
  *   d_table[v] = add_to[v] + scale * sum over r with tok_r = v of d_out_r
- * the sum in the order of the tokens (a row's in parts of at most 32, added in
+ * the sum in the order of the tokens (a row's in parts of at most 16, added in
  * order). Ids outside the
  * vocabulary have no row; one >= vocab sets the device error word.
  *   add_to            NULL (zero), or vocab x dim of table_dtype with d_table's

@@ -175,7 +175,7 @@ def test_embedding_grad(case):
 
 def test_embedding_grad_sums_in_the_order_of_the_tokens():
     # 1e8 + 1 - 1e8 ...: what fp32 makes of this depends on the order
-    rows = 30
+    rows = 15
     d = torch.tensor([1e8, 1.0, -1e8], device=DEV).repeat(rows // 3)[:, None].repeat(1, 4).contiguous()
     tokens = torch.full((rows,), 2, device=DEV)
     table = torch.empty(5, 4, device=DEV)
