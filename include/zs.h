@@ -678,9 +678,9 @@ zs_status zs_layer_norm_grad(const void* d_y, const void* x, zs_dtype dtype, int
  *                     the call returns.
  *   workspace         zs_grad_norm_workspace_bytes() bytes.
  *
- * zs_tensors_sqnorm — *sqnorm_out (device double) = the sum of all squares, each
- * fp32 group of 8 added in double; squares past fp32's range are summed in double
- * throughout. */
+ * zs_tensors_sqnorm — *sqnorm_out (device double) = the sum of all squares, of 8 or
+ * 16 neighbours in fp32 and then in double; in double throughout where fp32's range
+ * does not hold them. */
 zs_status zs_tensors_sqnorm(const void* const* tensors, const int64_t* numels, int32_t n,
                             zs_dtype dtype, void* workspace, int64_t workspace_bytes,
                             double* sqnorm_out, void* cuda_stream);
