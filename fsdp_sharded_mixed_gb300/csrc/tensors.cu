@@ -42,6 +42,7 @@ struct List {
   const void* in[MAXN];
   int64_t numel[MAXN];
   uint32_t first[MAXN + 1];  // chunks of the tensors before
+  uint16_t begin[kParts];    // the tensors that the blocks begin with
   uint8_t lead[MAXN];
   int32_t count;
 };
@@ -89,28 +90,54 @@ __device__ __forceinline__ float2 pair_at(const uint32_t* w, int i, __nv_bfloat1
   return {__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)};
 }
 
-// The sum of a unit's squares in fp32 (chains of eight at most), unless it left
-// fp32's range or is so small that squares may have: then in double.
+// The sum of a unit's squares in fp32, in two chains.
 template <typename T>
-__device__ __forceinline__ double squares(const uint32_t* w) {
+__device__ __forceinline__ float squares(const uint32_t* w) {
   float2 s = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < kPer<T> / 2; ++i) {
     const float2 v = pair_at(w, i, T());
     s = __ffma2_rn(v, v, s);
   }
-  const float sum = s.x + s.y;
-  if (sum > 1e-25f && sum < 1e37f) return sum;
-  uint32_t any = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) any |= w[i] & (sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
-  if (any == 0) return 0.0;
+  return s.x + s.y;
+}
+// The same in double, for units whose squares leave fp32's range.
+template <typename T>
+__device__ __forceinline__ double squares_wide(const uint32_t* w) {
   double d = 0.0;
 #pragma unroll
   for (int i = 0; i < kPer<T> / 2; ++i) {
     const float2 v = pair_at(w, i, T());
     d += (double)v.x * (double)v.x;
     d += (double)v.y * (double)v.y;
+  }
+  return d;
+}
+// A chunk's units: 16 elements of fp32 or 32 of bf16 go from fp32 to double as one
+// (double runs at a sixtieth of fp32's rate here: one conversion and addition a unit
+// kept its pipe 75 % busy and the norm of fp32 lists at 5.7 TB/s), unless their sum
+// is out of fp32's range, or so small that squares in it may have been: unit by unit.
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const uint32_t (*w)[8]) {
+  constexpr int kTogether = sizeof(T) == 4 ? kAtOnce : 2;
+  double d = 0.0;
+#pragma unroll
+  for (int j = 0; j < kAtOnce; j += kTogether) {
+    float s = squares<T>(w[j]) + squares<T>(w[j + 1]);
+    if (kTogether == 4) s += squares<T>(w[j + 2]) + squares<T>(w[j + 3]);
+    if (s > 1e-25f && s < 1e37f) {
+      d += (double)s;
+      continue;
+    }
+    uint32_t any = 0;
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        any |= w[j + u][i] & (sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu);
+    if (any == 0) continue;
+#pragma unroll
+    for (int u = 0; u < kTogether; ++u) d += squares_wide<T>(w[j + u]);
   }
   return d;
 }
@@ -136,9 +163,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   overlap_wait();
   const uint32_t chunks = a.list.first[a.list.count];
   double sum = 0.0;
-  int t = 0;
+  int t = a.list.begin[blockIdx.x];
   for (uint32_t c = blockIdx.x; c < chunks; c += kParts) {
-    t = tensor_of(a.list, c, t, a.list.count - 1);
     const int64_t numel = a.list.numel[t];
     const T* p = static_cast<const T*>(a.list.in[t]);
     const int64_t e0 = (int64_t)(c - a.list.first[t]) * kChunkUnits * kPer<T> - a.list.lead[t] +
@@ -153,8 +179,9 @@ __global__ void __launch_bounds__(kThreads, 4)
         load_edge(w[j], p, e, numel);
       }
     }
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) sum += squares<T>(w[j]);
+    // while they are on their way: the next chunk's tensor
+    if (c + kParts < chunks) t = tensor_of(a.list, c + kParts, t, a.list.count - 1);
+    sum += chunk_squares<T>(w);
   }
   __shared__ double warp_sums[kThreads / 32];
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_down_sync(0xFFFFFFFFu, sum, off);
@@ -166,26 +193,20 @@ __global__ void __launch_bounds__(kThreads, 4)
   a.partials[blockIdx.x] = b;
 }
 
-// The partials' sum, in one order; every thread gets it.
+// The partials' sum, in one order, by the first warp (whose lanes get it).
 __device__ __forceinline__ double total_of(const double* partials) {
-  __shared__ double warp_sums[kThreads / 32];
-  double t = 0.0, p[(kParts + kThreads - 1) / kThreads];
+  constexpr int kEach = kParts / 32;
+  static_assert(kParts % 32 == 0, "every lane takes as many");
+  double t = 0.0, p[kEach];
 #pragma unroll
-  for (int k = 0; k < (kParts + kThreads - 1) / kThreads; ++k) {
-    const int b = threadIdx.x + k * kThreads;
-    p[k] = b < kParts ? __ldcg(partials + b) : 0.0;
-  }
+  for (int k = 0; k < kEach; ++k) p[k] = __ldcg(partials + threadIdx.x % 32 + 32 * k);
 #pragma unroll
-  for (int k = 0; k < (kParts + kThreads - 1) / kThreads; ++k) t += p[k];
-  for (int off = 16; off > 0; off >>= 1) t += __shfl_down_sync(0xFFFFFFFFu, t, off);
-  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = t;
-  __syncthreads();
-  t = 0.0;
-  for (int w = 0; w < kThreads / 32; ++w) t += warp_sums[w];
+  for (int k = 0; k < kEach; ++k) t += p[k];
+  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, off);
   return t;
 }
 
-__global__ void __launch_bounds__(kThreads) join_norm_kernel(const double* partials, double* out) {
+__global__ void __launch_bounds__(32) join_norm_kernel(const double* partials, double* out) {
   overlap_wait();
   const double total = total_of(partials);
   if (threadIdx.x == 0) *out = total;
@@ -249,29 +270,16 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16* q, const float2* v, in
 template <typename T, typename OT, int MAXN>
 __global__ void __launch_bounds__(kThreads, 4)
     list_scale_kernel(const __grid_constant__ ScaleArgs<MAXN> a) {
+  __shared__ float shared_coef;
+  __shared__ bool shared_skip;
   overlap_wait();
-  float coef;
-  if (a.coef) {
-    if (a.skip && *a.skip) return;
-    coef = *a.coef;
-  } else {
-    const double norm = sqrt(total_of(a.partials)), c = a.max_norm / (norm + 1e-6);
-    const bool bad = !isfinite(norm);
-    coef = bad ? 1.0f : (float)(c < 1.0 ? c : 1.0);
-    if (a.norm_out && blockIdx.x == 0 && threadIdx.x == 0) {
-      *a.norm_out = (float)norm;
-      *a.coef_out = coef;
-      *a.nonfinite_out = bad ? 1 : 0;
-    }
-    if (bad) return;
-  }
+  float coef = 1.0f;
+  bool known = false;  // the coefficient: found out while the first loads are on their way
   const uint32_t chunks = a.list.first[a.list.count];
-  int t = a.list.count - 1;
-  for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+  int t = a.list.begin[blockIdx.x];
+  for (uint32_t k = blockIdx.x; k < chunks || !known; k += gridDim.x) {
     const uint32_t c = chunks - 1 - k;
-    t = tensor_of(a.list, c, 0, t);
-    if (coef == 1.0f && a.list.in[t] == a.out[t]) continue;  // in place: nothing changes
-    const int64_t numel = a.list.numel[t];
+    const int64_t numel = k < chunks ? a.list.numel[t] : 0;
     const T* p = static_cast<const T*>(a.list.in[t]);
     OT* q = static_cast<OT*>(a.out[t]);
     const int64_t e0 = (int64_t)(c - a.list.first[t]) * kChunkUnits * kPer<T> - a.list.lead[t] +
@@ -289,6 +297,33 @@ __global__ void __launch_bounds__(kThreads, 4)
         load_edge(w[j], p, e, numel);
       }
     }
+    const bool same = (const void*)p == (const void*)q;
+    if (k + gridDim.x < chunks) t = tensor_of(a.list, c - gridDim.x, 0, t);
+    if (!known) {
+      known = true;
+      if (a.coef) {
+        if (a.skip && *a.skip) return;
+        coef = *a.coef;
+      } else {
+        if (threadIdx.x < 32) {
+          const double total = total_of(a.partials);
+          if (threadIdx.x == 0) {
+            const double norm = sqrt(total), c = a.max_norm / (norm + 1e-6);
+            shared_skip = !isfinite(norm);
+            shared_coef = shared_skip ? 1.0f : (float)(c < 1.0 ? c : 1.0);
+            if (a.norm_out && blockIdx.x == 0) {
+              *a.norm_out = (float)norm;
+              *a.coef_out = shared_coef;
+              *a.nonfinite_out = shared_skip ? 1 : 0;
+            }
+          }
+        }
+        __syncthreads();
+        if (shared_skip) return;
+        coef = shared_coef;
+      }
+    }
+    if (coef == 1.0f && same) continue;  // in place: nothing changes
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       const int64_t e = e0 + j * (kThreads * kPer<T>);
@@ -310,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 constexpr int kMostListed = 768;  // tensors of one launch
 
 // Fills the list with tensors [from, from + n) of a call's that hold something.
-// units_of: the bytes that a unit's first element is aligned to, and the addresses.
+// From the list's end (the scaling), block b of `blocks` begins with chunk b from there.
 template <int MAXN>
 void fill_list(List<MAXN>* l, const TensorsLaunch& in, int64_t from, int n, void** out) {
   const int es = in.dtype == ZS_BF16 ? 2 : 4, per = kUnitBytes / es;
@@ -329,6 +364,15 @@ void fill_list(List<MAXN>* l, const TensorsLaunch& in, int64_t from, int n, void
     l->lead[k] = (uint8_t)(at % align / os);
     const int64_t units = (l->lead[k] + in.numels[i] + per - 1) / per;
     l->first[k + 1] = l->first[k] + (uint32_t)((units + kChunkUnits - 1) / kChunkUnits);
+  }
+  const uint32_t chunks = l->first[l->count];
+  int t = out && l->count > 0 ? l->count - 1 : 0;
+  for (uint32_t b = 0; b < (uint32_t)kParts; ++b) {
+    if (b < chunks && !out)
+      while (l->first[t + 1] <= b) ++t;
+    if (b < chunks && out)
+      while (l->first[t] > chunks - 1 - b) --t;
+    l->begin[b] = (uint16_t)t;
   }
 }
 
@@ -401,7 +445,7 @@ cudaError_t launch_tensors(const TensorsLaunch& in, bool norm, bool scale, cudaS
                  [&](int64_t f, int n) { return launch_norm_of<256>(in, f, n, stream); },
                  [&](int64_t f, int n) { return launch_norm_of<kMostListed>(in, f, n, stream); });
   if (e == cudaSuccess && norm && in.sqnorm)
-    e = launch_kernel(join_norm_kernel, dim3(1), dim3(kThreads), 0, stream,
+    e = launch_kernel(join_norm_kernel, dim3(1), dim3(32), 0, stream,
                       static_cast<const double*>(in.workspace), in.sqnorm);
   if (e != cudaSuccess || !scale) return e;
   return in_parts(in, [&](int64_t f, int n) { return launch_scale_of<64>(in, f, n, stream); },
