@@ -90,7 +90,22 @@ __device__ __forceinline__ void load_words(uint32_t* w, const void* p) {
   }
 }
 template <int N>
-__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w, bool once = false) {
+  if (once) {  // L2 is told to let it go first
+    if (N == 8 && (uintptr_t)p % 32 == 0) {
+      asm volatile("st.global.L2::evict_first.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[N - 4]), "r"(w[N - 3]),
+                   "r"(w[N - 2]), "r"(w[N - 1])
+                   : "memory");
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(static_cast<uint4*>(p) + i),
+                   "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                   : "memory");
+    return;
+  }
   if (N == 8 && (uintptr_t)p % 32 == 0) {
     asm volatile("st.global.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[N - 4]), "r"(w[N - 3]), "r"(w[N - 2]),
@@ -128,10 +143,11 @@ __device__ __forceinline__ Raw8<T> load8(const T* row, int col0, int lane, int D
 }
 
 template <typename T, Lay LAY>
-__device__ __forceinline__ void store_raw8(T* row, int col0, int lane, int D, const Raw8<T>& r) {
+__device__ __forceinline__ void store_raw8(T* row, int col0, int lane, int D, const Raw8<T>& r,
+                                           bool once = false) {
   constexpr int kWords = kLane * (int)sizeof(T) / 4;
   if (LAY == kEight && col0 + lane * 8 + 8 <= D) {
-    store_words<kWords>(row + col0 + lane * 8, r.w);
+    store_words<kWords>(row + col0 + lane * 8, r.w, once);
     return;
   }
   if (LAY == kFour && col0 + 128 + lane * 4 + 4 <= D) {
@@ -147,7 +163,8 @@ __device__ __forceinline__ void store_raw8(T* row, int col0, int lane, int D, co
 }
 
 template <typename T, Lay LAY>
-__device__ __forceinline__ void store8(T* row, int col0, int lane, int D, const float* v) {
+__device__ __forceinline__ void store8(T* row, int col0, int lane, int D, const float* v,
+                                       bool once = false) {
   Raw8<T> r;
 #pragma unroll
   for (int k = 0; k < kLane; ++k) {
@@ -155,7 +172,7 @@ __device__ __forceinline__ void store8(T* row, int col0, int lane, int D, const 
     put(&x, v[k]);
     set_raw(r, k, x);
   }
-  store_raw8<T, LAY>(row, col0, lane, D, r);
+  store_raw8<T, LAY>(row, col0, lane, D, r, once);
 }
 
 // A lane's elements two by two, for the packed fp32 arithmetic.
