@@ -7,11 +7,11 @@ output head, vocabulary 1000, width 256); the teacher a fixed table of logits
 for the token that follows. Each step, every rank
   1. records its tokens' 16 most likely successors by the teacher
      (zs_token_logprobs: ids and log probabilities),
-  2. takes the loss against that record mixed with the hard labels', and its
-     gradient, in one pass over the student's logits, in place
-     (zs_distill_loss_grad),
-  3. turns it into its flat bf16 gradient (the model's own backward pass; the
-     matrix products are torch's),
+  2. looks its tokens up in the embedding (zs_embedding) and takes the loss against
+     that record mixed with the hard labels', and its gradient, in one pass over the
+     student's logits, in place (zs_distill_loss_grad),
+  3. turns it into its flat bf16 gradient: the embedding's by sorted tokens, straight
+     into its place (zs_embedding_grad), the head's by a matrix product (torch's),
 and then every rank's zs_shard_step takes the mean of the ranks' slices of its
 shard, updates it with AdamW and casts it into the flat parameter buffer, whose
 views are the student's weights for the next step.
@@ -61,6 +61,9 @@ def main(steps=60, log=print):
     record = torch.empty(TOKENS, TOP, **f32)
     zero_lse = torch.zeros(TOKENS, **f32)   # the record holds log probabilities already
     loss, logprob, entropy = (torch.empty(TOKENS, **f32) for _ in range(3))
+    hidden = torch.empty(TOKENS, WIDTH, dtype=torch.bfloat16, device=dev)
+    scratch = torch.empty(zs.zs_embedding_grad_workspace_bytes(TOKENS, WIDTH), dtype=torch.uint8,
+                          device=dev)
     w_soft = torch.full((TOKENS,), SOFT / TOKENS, **f32)
     w_hard = torch.full((TOKENS,), -HARD / TOKENS, **f32)   # of the log probability
 
@@ -69,11 +72,16 @@ def main(steps=60, log=print):
         following = torch.multinomial(torch.softmax(teacher[tokens], 1), 1, generator=g)[:, 0]
         return tokens, following
 
+    def look_up(tokens):
+        zs.zs_embedding(embed, zs.ZS_BF16, VOCAB, WIDTH, WIDTH, tokens, TOKENS, 1.0, hidden,
+                        zs.ZS_BF16, WIDTH)
+        return hidden
+
     held_out = batch()
 
     def evaluate():
         tokens, following = held_out
-        torch.mm(embed[tokens], head.t(), out=logits)
+        torch.mm(look_up(tokens), head.t(), out=logits)
         zs.zs_token_logprobs(logits, zs.ZS_BF16, TOKENS, VOCAB, VOCAB, following, 1.0, logprob,
                              entropy)
         return logprob.mean().item(), entropy.mean().item()
@@ -87,16 +95,14 @@ def main(steps=60, log=print):
             tokens, following = batch()
             zs.zs_token_logprobs(teacher[tokens], zs.ZS_FP32, TOKENS, VOCAB, VOCAB, None, 1.0,
                                  top_k=TOP, top_ids=ids, top_logprobs=record)
-            hidden = embed[tokens]
-            torch.mm(hidden, head.t(), out=logits)
+            torch.mm(look_up(tokens), head.t(), out=logits)
             zs.zs_distill_loss_grad(logits, zs.ZS_BF16, TOKENS, VOCAB, VOCAB, ids, record,
                                     zs.ZS_FP32, TOP, zero_lse, 1.0, following, w_soft, w_hard,
                                     loss, None, logprob, None, logits, VOCAB)
             total += loss.mean().item()
-            d_embed = torch.zeros(VOCAB, WIDTH, **f32)
-            d_embed.index_add_(0, tokens, (logits @ head).float())
             flat = grads[rank]
-            flat[:VOCAB * WIDTH] = d_embed.flatten()
+            zs.zs_embedding_grad(logits @ head, zs.ZS_BF16, TOKENS, WIDTH, WIDTH, tokens, VOCAB,
+                                 1.0, None, scratch, flat[:VOCAB * WIDTH], zs.ZS_BF16, WIDTH)
             flat[VOCAB * WIDTH:plan.P] = (logits.t() @ hidden).flatten()
         for rank, state in enumerate(shards):
             slices = [flat.narrow(0, rank * S, S) for flat in grads]
