@@ -308,7 +308,8 @@ struct Reduce {
   static constexpr int kWords = kLane / 4 * ((int)sizeof(T) + (ADD ? (int)sizeof(GT) : 0));
   static constexpr int kRows = kWords <= 4 ? 16 : 8;  // on their way at once
   const GradArgs& a;
-  const int lane, col0;
+  const int lane;
+  int col0;
   float2 acc[kLane / 2];
   Raw8<GT> base;
 
@@ -544,6 +545,151 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   }
 }
 
+// ---- few tokens -------------------------------------------------------------------
+// One launch: block b owns rows b, b + B, ... of the table. It picks its tokens from
+// the batch, ranks them by row (counting, in order), writes its rows without tokens
+// and sums the others, 16 tokens a part. For batches whose tokens a block reads at a
+// glance, and whose rows it could sum alone if all went to one of the table's.
+constexpr int kFewTokens = 1024;
+constexpr int kFewItems = 2048;  // tokens times slabs
+constexpr int kFewBlocks = 304;  // two to an SM of 152
+struct FewShared {
+  uint32_t row[kFewTokens], token[kFewTokens];    // the block's, as they come
+  uint32_t sorted_row[kFewTokens], sorted[kFewTokens];
+  int begin[kFewTokens + 1];                      // of the runs of one row
+  int count, runs;
+  uint32_t met[(ZS_MAX_VOCAB / kFewBlocks + 32) / 32];  // the block's rows with tokens
+  float2 parts[kWarps][kLane / 2][32];
+};
+
+template <typename T, typename GT, Lay LAY, bool ADD>
+__global__ void __launch_bounds__(kThreads, 2)
+    few_tokens_kernel(const __grid_constant__ GradArgs a, const int64_t* tokens, bool fill) {
+  using R = Reduce<T, GT, LAY, ADD>;
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  __shared__ FewShared sh;
+  overlap_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const uint32_t B = gridDim.x, me = blockIdx.x;
+  for (int i = tid; i < (int)(sizeof(sh.met) / 4); i += kThreads) sh.met[i] = 0;
+  if (tid == 0) sh.count = 0;
+  __syncthreads();
+  // Its tokens, 32 at a time, each warp those of its share (they are put in order below).
+  for (int t = tid; t < (int)a.rows; t += kThreads) {
+    const int64_t v = tokens[t];
+    if (v >= a.vocab && me == 0) atomicOr(a.err, 4u);
+    if (v < 0 || v >= a.vocab || (uint32_t)v % B != me) continue;
+    const int at = atomicAdd(&sh.count, 1);
+    if (!within(at, at + 1, 0, kFewTokens, a.err)) continue;
+    sh.row[at] = (uint32_t)v;
+    sh.token[at] = (uint32_t)t;
+    const uint32_t i = (uint32_t)v / B;
+    if (fill) atomicOr(&sh.met[i / 32], 1u << (i & 31));
+  }
+  __syncthreads();
+  const int n = sh.count;
+  // by row, then by token (unique, so that the order they were listed in is nothing)
+  for (int j = tid; j < n; j += kThreads) {
+    const uint64_t mine = (uint64_t)sh.row[j] << 32 | sh.token[j];
+    int place = 0;
+    for (int i = 0; i < n; ++i) place += ((uint64_t)sh.row[i] << 32 | sh.token[i]) < mine;
+    sh.sorted_row[place] = (uint32_t)(mine >> 32);
+    sh.sorted[place] = (uint32_t)mine;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int runs = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const bool first = i < n && (i == 0 || sh.sorted_row[i] != sh.sorted_row[i - 1]);
+      const uint32_t firsts = __ballot_sync(kAll, first);
+      if (first) sh.begin[runs + __popc(firsts & ((1u << lane) - 1))] = i;
+      runs += __popc(firsts);
+    }
+    if (lane == 0) {
+      sh.begin[runs] = n;
+      sh.runs = runs;
+    }
+  }
+  __syncthreads();
+  const int runs = sh.runs;
+  R r{a, lane, 0, {}, {}};
+  // The sum of sorted tokens [from, to).
+  auto sum = [&](int from, int to) {
+    r.clear();
+    for (int i0 = from; i0 < to; i0 += R::kRows) {
+      Raw8<T> rows[R::kRows];
+#pragma unroll
+      for (int u = 0; u < R::kRows; ++u)
+        if (i0 + u < to) rows[u] = r.row(sh.sorted[i0 + u]);
+#pragma unroll
+      for (int u = 0; u < R::kRows; ++u)
+        if (i0 + u < to) r.add(rows[u]);
+    }
+  };
+  // Rows of a part, a warp to a slab each.
+  for (int u = warp; u < runs * a.slabs; u += kWarps) {
+    const int run = u / a.slabs, from = sh.begin[run], to = sh.begin[run + 1];
+    if (to - from > kEach) continue;
+    r.col0 = (u - run * a.slabs) * kSlab;
+    const uint32_t v = sh.sorted_row[from];
+    if (ADD) r.base = r.base_of(v);
+    sum(from, to);
+    r.write(v);
+  }
+  // Rows of more, the block together: a part a warp, added in order by the first.
+  for (int run = 0; run < runs; ++run) {
+    const int from = sh.begin[run], to = sh.begin[run + 1];
+    if (to - from <= kEach) continue;
+    const uint32_t v = sh.sorted_row[from];
+    for (int slab = 0; slab < a.slabs; ++slab) {
+      r.col0 = slab * kSlab;
+      float2 total[kLane / 2] = {};
+      for (int p0 = from; p0 < to; p0 += kWarps * kEach) {
+        const int p = p0 + warp * kEach;
+        if (p < to) {
+          sum(p, min(to, p + kEach));
+          r.keep(sh.parts[warp]);
+        }
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int i = 0; i < kLane / 2; ++i) r.acc[i] = total[i];
+          for (int w = 0; w < kWarps && p0 + w * kEach < to; ++w) r.add_kept(sh.parts[w]);
+#pragma unroll
+          for (int i = 0; i < kLane / 2; ++i) total[i] = r.acc[i];
+        }
+        __syncthreads();
+      }
+      if (warp == 0) {
+        if (ADD) r.base = r.base_of(v);
+        r.write(v);
+      }
+    }
+  }
+  // The rows without tokens: zero, or what the gradient is added to.
+  if (!fill) return;
+  for (uint32_t i = warp; i * (int64_t)B + me < a.vocab; i += kWarps) {
+    if (sh.met[i / 32] >> (i & 31) & 1) continue;
+    const int64_t v = i * (int64_t)B + me;
+    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
+    GT* to = static_cast<GT*>(a.d_table) + v * a.table_stride;
+    const GT* from = static_cast<const GT*>(a.add) + v * a.table_stride;
+    constexpr int kSlabs = 4;
+    for (int s0 = 0; s0 < a.slabs; s0 += kSlabs) {
+      Raw8<GT> x[kSlabs];
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s) {
+        x[s] = {};
+        if (ADD && s0 + s < a.slabs) x[s] = load8<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
+      }
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s)
+        if (s0 + s < a.slabs) store_raw8<GT, LAY>(to, (s0 + s) * kSlab, lane, a.dim, x[s]);
+    }
+  }
+}
+
 template <typename TT, typename OT>
 cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
   const dim3 grid((unsigned)((a.rows + kWarps - 1) / kWarps),
@@ -583,6 +729,14 @@ cudaError_t clusters_at_once(const void* kernel, int* n) {
 template <typename T, typename GT, Lay LAY>
 cudaError_t launch_sums(const SortArgs& k, const GradArgs& a, cudaStream_t stream) {
   const bool fill = a.add != a.d_table;
+  if (k.rows > 0 && k.rows <= kFewTokens && k.rows * a.slabs <= kFewItems) {
+    // as many blocks as there are rows for their warps, or tokens
+    const int64_t work = fill ? (a.vocab + kWarps - 1) / kWarps : k.rows;
+    const int64_t blocks = work < kFewBlocks ? work : kFewBlocks;
+    return launch_kernel(a.add ? few_tokens_kernel<T, GT, LAY, true>
+                               : few_tokens_kernel<T, GT, LAY, false>,
+                         dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, k.tokens, fill);
+  }
   if (k.rows > 0 || fill) {
     auto* kernel = sort_and_fill_kernel<GT, LAY>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

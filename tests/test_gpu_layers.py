@@ -128,6 +128,11 @@ GRADS = [  # rows, vocab, dim, d_out dtype, table dtype, pads, offsets, tokens, 
     (5000, 1023, 130, F, F, 3, 5, 1, 2, "zipf", None),
     (100, 2, 32768, B, F, 0, 0, 0, 0, "two", None),
     (257, zs.ZS_MAX_VOCAB, 8, B, B, 0, 0, 0, 0, "any", None),
+    (2100, 12, 300, B, F, 4, 4, 0, 0, "blocks", "other"),
+    (2100, 12, 100, F, B, 0, 0, 0, 0, "blocks", "self"), (1025, 7, 40, F, F, 0, 0, 0, 0, "any", None),
+    (1500, 5, 256, B, F, 0, 0, 0, 0, "same", "self"), (4000, 50, 65, F, F, 0, 0, 0, 0, "two", None),
+    (1024, 3, 512, B, B, 0, 0, 0, 0, "same", "other"), (1024, 900, 8, B, F, 0, 0, 0, 0, "zipf", None),
+    (3, zs.ZS_MAX_VOCAB, 8, F, B, 0, 0, 0, 0, "any", "self"),
     (40000, 3000, 64, F, F, 0, 0, 0, 0, "zipf", None), (40, 9, 16, F, F, 0, 0, 0, 0, "none", "other"),
     (0, 9, 16, F, B, 0, 0, 0, 0, "any", None), (0, 9, 16, F, B, 0, 0, 0, 0, "any", "other"),
     (0, 9, 16, F, B, 0, 0, 0, 0, "any", "self"),
