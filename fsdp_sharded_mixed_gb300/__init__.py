@@ -566,6 +566,12 @@ def _rows_ptr(x, rows, vocab, stride, dtype, fn, name):
     if x is None or isinstance(x, int):
         return x
     size = ELEM_BYTES.get(dtype, 0)
+    need = ((rows - 1) * stride + vocab) * size if rows > 0 else 0
+    try:
+        if x.is_contiguous() and x.nbytes >= need:  # a dense tensor that is long enough
+            return x.data_ptr()
+    except AttributeError:  # a numpy array
+        pass
     if hasattr(x, "data_ptr") and not x.is_contiguous():
         if x.dim() != 2 or x.stride(1) != 1 or x.stride(0) != stride \
                 or x.element_size() != size:
@@ -573,7 +579,7 @@ def _rows_ptr(x, rows, vocab, stride, dtype, fn, name):
         if x.shape[0] < rows or x.shape[1] < vocab:
             raise ValueError(f"{fn}: {name} is {tuple(x.shape)}, the call needs {(rows, vocab)}")
         return x.data_ptr()
-    return _row_ptr(x, ((rows - 1) * stride + vocab) * size if rows > 0 else 0, fn, name)
+    return _row_ptr(x, need, fn, name)
 
 
 def _row_ptr(x, nbytes, fn, name):

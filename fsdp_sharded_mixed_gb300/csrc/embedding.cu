@@ -6,7 +6,7 @@
 //
 // The gradient sorts the tokens (a stable counting sort, so that a row's sum
 // runs over its tokens in their order) and then takes the sorted positions in
-// blocks of 256, 16 a warp, for a slab of 256 columns. A run of equal tokens
+// blocks of 128, 16 a warp, for a slab of 256 columns. A run of equal tokens
 // within a warp's 16 is summed by it; the parts of longer ones and of those that
 // cross warps are added in their order, through shared memory and, across blocks,
 // scratch memory. So the work of a warp is bounded however often a token occurs,
@@ -14,8 +14,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-
-#include <atomic>
 
 #include "bounds.cuh"
 #include "overlap.cuh"
@@ -93,10 +91,12 @@ struct SortArgs {
   uint32_t* tickets;         // cleared for the reduction
   int64_t rows, n_tickets, share;  // share: tokens of a warp
   int32_t vocab, passes, bits;
+  unsigned int* err;
 };
 
 struct GradArgs {
   const void* d_out;
+  const int64_t* tokens;
   const void* add;    // or NULL
   void* d_table;
   const uint32_t *keys, *order;
@@ -104,6 +104,7 @@ struct GradArgs {
   uint32_t* tickets;  // [slabs][blocks]
   int64_t rows, blocks, row_stride, table_stride;
   int32_t vocab, dim, slabs, part_dim;
+  int32_t fill_blocks;  // of the launch, which write the rows without tokens
   float scale;
   unsigned int* err;
 };
@@ -223,70 +224,48 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
   }
 }
 
-// Rows of the table: zero, or what the gradient is added to.
-constexpr int kFillBytes = 32 * 1024;  // of a dense table, a block at a time
-template <typename GT, Lay LAY>
-__device__ void fill_rows(const GradArgs& a, int64_t block, int64_t blocks) {
-  const int lane = threadIdx.x & 31;
-  if (LAY != kOne && a.table_stride == a.dim && ((uintptr_t)a.d_table | (uintptr_t)a.add) % 32 == 0) {
-    // dense: 32 bytes a thread, four times over
-    const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT), whole = bytes / 32 * 32;
-    unsigned char* to = static_cast<unsigned char*>(a.d_table);
-    const unsigned char* from = static_cast<const unsigned char*>(a.add);
-    constexpr int kAtOnce = 4;
-    for (int64_t i0 = block * kAtOnce * kFillBytes + threadIdx.x * 32; i0 < whole;
-         i0 += blocks * kAtOnce * kFillBytes) {
-      uint32_t w[kAtOnce][8] = {};
-      if (from)
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int64_t i = i0 + u * kFillBytes;
-          if (i < whole && within(i, i + 32, 0, bytes, a.err)) load_words<8>(w[u], from + i);
-        }
-#pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) {
-        const int64_t i = i0 + u * kFillBytes;
-        if (i < whole && within(i, i + 32, 0, bytes, a.err)) store_words<8>(to + i, w[u]);
-      }
-    }
-    for (int64_t i = whole + threadIdx.x * (int)sizeof(GT); block == 0 && i < bytes;
-         i += kSortThreads * (int)sizeof(GT)) {
-      const GT* p = reinterpret_cast<const GT*>(from + i);
-      *reinterpret_cast<GT*>(to + i) = from ? *p : GT(0.0f);
-    }
-    return;
-  }
-  for (int64_t v = block * kSortWarps + threadIdx.x / 32; v < a.vocab; v += blocks * kSortWarps) {
-    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
-    GT* row = static_cast<GT*>(a.d_table) + v * a.table_stride;
-    const GT* add = a.add ? static_cast<const GT*>(a.add) + v * a.table_stride : nullptr;
-    for (int col0 = 0; col0 < a.dim; col0 += kSlab) {
-      Raw8<GT> r = {};
-      if (add) r = load8<GT, LAY>(add, col0, lane, a.dim);
-      store_raw8<GT, LAY>(row, col0, lane, a.dim, r);
-    }
-  }
-}
-
-// The first cluster sorts the tokens (where there are any); the others write the
-// rows meanwhile, those of the batch's tokens too, which the sums write again.
-template <typename GT, Lay LAY>
 __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks, 1, 1)
-    sort_and_fill_kernel(const __grid_constant__ SortArgs a, const __grid_constant__ GradArgs g) {
+    sort_tokens_kernel(const __grid_constant__ SortArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   overlap_wait();
-  const int sorting = a.rows > 0 ? kSortBlocks : 0;
-  if ((int)blockIdx.x < sorting)
-    sort_tokens(a, *reinterpret_cast<SortShared*>(smem), (int)blockIdx.x, g.err);
-  else
-    fill_rows<GT, LAY>(g, (int64_t)blockIdx.x - sorting, (int64_t)gridDim.x - sorting);
+  sort_tokens(a, *reinterpret_cast<SortShared*>(smem), (int)blockIdx.x, a.err);
+}
+
+// ---- rows without tokens ----------------------------------------------------------
+// Block b of B owns rows b, b + B, ... of the table; `met` has a bit for each of them,
+// set where the batch has tokens of it.
+constexpr int kFillBlocks = 304;  // two to an SM of 152
+constexpr int kMetWords = (ZS_MAX_VOCAB / kFillBlocks + 32) / 32;
+
+// Zero, or what the gradient is added to: a warp to a row.
+template <typename GT, Lay LAY, bool ADD>
+__device__ __forceinline__ void fill_rows(const GradArgs& a, const uint32_t* met, uint32_t me,
+                                          uint32_t B) {
+  const int lane = threadIdx.x & 31;
+  for (uint32_t i = threadIdx.x / 32; i * (int64_t)B + me < a.vocab; i += kWarps) {
+    if (met[i / 32] >> (i & 31) & 1) continue;
+    const int64_t v = i * (int64_t)B + me;
+    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
+    GT* to = static_cast<GT*>(a.d_table) + v * a.table_stride;
+    const GT* from = static_cast<const GT*>(a.add) + v * a.table_stride;
+    constexpr int kSlabs = 4;
+    for (int s0 = 0; s0 < a.slabs; s0 += kSlabs) {
+      Raw8<GT> x[kSlabs];
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s) {
+        x[s] = {};
+        if (ADD && s0 + s < a.slabs) x[s] = load8<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
+      }
+#pragma unroll
+      for (int s = 0; s < kSlabs; ++s)
+        if (s0 + s < a.slabs) store_raw8<GT, LAY>(to, (s0 + s) * kSlab, lane, a.dim, x[s]);
+    }
+  }
 }
 
 // ---- sums over sorted tokens -----------------------------------------------------
-constexpr int kSumThreads = 512;
-constexpr int kSumWarps = kSumThreads / 32;
-constexpr int kEach = 16;                   // sorted positions of a warp
-constexpr int kBlock = kEach * kSumWarps;  // and of a block
+constexpr int kEach = 16;               // sorted positions of a warp
+constexpr int kBlock = kEach * kWarps;  // and of a block
 
 // What a warp of a block knows of its first and its last run.
 struct Edges {
@@ -297,16 +276,16 @@ struct Edges {
 // The parts of runs that cross warps: of the first run, if it began before, and of
 // the last, if it goes on.
 struct Crossing {
-  Edges edges[kSumWarps];
+  Edges edges[kWarps];
   int64_t from[2], to[2];  // of the block's first run and its last, where they cross blocks
-  float2 parts[kSumWarps][2][kLane / 2][32];
+  float2 parts[kWarps][2][kLane / 2][32];
 };
 
 // ADD: the sums are added to something.
 template <typename T, typename GT, Lay LAY, bool ADD>
 struct Reduce {
   static constexpr int kWords = kLane / 4 * ((int)sizeof(T) + (ADD ? (int)sizeof(GT) : 0));
-  static constexpr int kRows = kWords <= 4 ? 16 : 8;  // on their way at once
+  static constexpr int kRows = kWords <= 4 ? 8 : kWords <= 8 ? 4 : 2;  // on their way at once
   const GradArgs& a;
   const int lane;
   int col0;
@@ -362,7 +341,7 @@ struct Reduce {
   }
   // The parts of blocks from..to of one run, in their order.
   __device__ __forceinline__ void add_parts(int64_t from, int64_t to) {
-    constexpr int kAtOnce = 8;
+    constexpr int kAtOnce = 4;
     for (int64_t j0 = from; j0 <= to; j0 += kAtOnce) {
       Raw8<float> r[kAtOnce];
 #pragma unroll
@@ -418,16 +397,12 @@ __device__ __forceinline__ void run_of(const GradArgs& a, uint32_t v, int lane, 
 // warp in which they start, those that cross blocks from scratch memory by the
 // block that is through with its part last.
 template <typename T, typename GT, Lay LAY, bool ADD>
-__global__ void __launch_bounds__(kSumThreads, 1)
-    sum_tokens_kernel(const __grid_constant__ GradArgs a) {
+__device__ __forceinline__ void sum_tokens(const GradArgs& a, Crossing& sh, int64_t item) {
   using R = Reduce<T, GT, LAY, ADD>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  extern __shared__ __align__(16) unsigned char smem[];
-  Crossing& sh = *reinterpret_cast<Crossing*>(smem);
-  overlap_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t b = blockIdx.x / a.slabs;
-  const int slab = (int)(blockIdx.x - b * a.slabs);
+  const int64_t b = item / a.slabs;
+  const int slab = (int)(item - b * a.slabs);
   const int64_t p0 = b * kBlock + warp * kEach;
   // the warp's keys, and one to either side
   const int64_t p = lane == 31 ? p0 - 1 : p0 + lane;
@@ -463,7 +438,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       if (ADD && (starts >> i & 1)) bases[ADD ? u : 0] = r.base_of(__shfl_sync(kAll, here, i));
     }
     // while they are on their way: how far the runs that cross the block's ends go
-    if (i0 == 0 && ((warp == 0 && e.from_before) || (warp == kSumWarps - 1 && e.to_next))) {
+    if (i0 == 0 && ((warp == 0 && e.from_before) || (warp == kWarps - 1 && e.to_next))) {
       const int end = warp == 0 && e.from_before ? 0 : 1;
       int64_t from, to;
       run_of(a, end ? e.v_last : e.v_first, lane, &from, &to);
@@ -504,7 +479,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 
   // Adds the parts of a run from warp w on; whether it ends within the block.
   auto add_from = [&](int w) {
-    for (; w < kSumWarps; ++w) {
+    for (; w < kWarps; ++w) {
       r.add_kept(sh.parts[w][0]);
       if (!sh.edges[w].one || !sh.edges[w].to_next) return true;
     }
@@ -545,6 +520,40 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   }
 }
 
+// The first blocks write the rows without tokens, which they see from the tokens
+// themselves; the others take a block of sorted positions and a slab each, and
+// three blocks share an SM, so that the sums run beside the writing. The launch
+// follows the sort's, but only the sums wait for that: the rows are written while it
+// runs. (What came before the sort has ended by then: the sort waited for it before
+// it let this launch start.)
+template <typename T, typename GT, Lay LAY, bool ADD>
+__global__ void __launch_bounds__(kThreads, 3)
+    embedding_grad_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ union {
+    Crossing sums;
+    uint32_t met[kMetWords];
+  } sh;
+  if ((int)blockIdx.x >= a.fill_blocks) {
+    overlap_wait();
+    sum_tokens<T, GT, LAY, ADD>(a, sh.sums, (int64_t)blockIdx.x - a.fill_blocks);
+    return;
+  }
+  if (a.rows == 0) overlap_wait();  // there is no sort
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int i = threadIdx.x; i < kMetWords; i += kThreads) sh.met[i] = 0;
+  __syncthreads();
+  const uint32_t B = a.fill_blocks, me = blockIdx.x;
+#pragma unroll 8
+  for (int64_t t = threadIdx.x; t < a.rows; t += kThreads) {
+    const int64_t v = __ldcg(reinterpret_cast<const long long*>(a.tokens) + t);
+    if (v < 0 || v >= a.vocab || (uint32_t)v % B != me) continue;
+    const uint32_t i = (uint32_t)v / B;
+    atomicOr(&sh.met[i / 32], 1u << (i & 31));
+  }
+  __syncthreads();
+  fill_rows<GT, LAY, ADD>(a, sh.met, me, B);
+}
+
 // ---- few tokens -------------------------------------------------------------------
 // One launch: block b owns rows b, b + B, ... of the table. It picks its tokens from
 // the batch, ranks them by row (counting, in order), writes its rows without tokens
@@ -552,31 +561,31 @@ __global__ void __launch_bounds__(kSumThreads, 1)
 // glance, and whose rows it could sum alone if all went to one of the table's.
 constexpr int kFewTokens = 1024;
 constexpr int kFewItems = 2048;  // tokens times slabs
-constexpr int kFewBlocks = 304;  // two to an SM of 152
 struct FewShared {
   uint32_t row[kFewTokens], token[kFewTokens];    // the block's, as they come
   uint32_t sorted_row[kFewTokens], sorted[kFewTokens];
   int begin[kFewTokens + 1];                      // of the runs of one row
   int count, runs;
-  uint32_t met[(ZS_MAX_VOCAB / kFewBlocks + 32) / 32];  // the block's rows with tokens
+  uint32_t met[kMetWords];
   float2 parts[kWarps][kLane / 2][32];
 };
 
 template <typename T, typename GT, Lay LAY, bool ADD>
 __global__ void __launch_bounds__(kThreads, 2)
-    few_tokens_kernel(const __grid_constant__ GradArgs a, const int64_t* tokens, bool fill) {
+    few_tokens_kernel(const __grid_constant__ GradArgs a) {
   using R = Reduce<T, GT, LAY, ADD>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
   __shared__ FewShared sh;
   overlap_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const uint32_t B = gridDim.x, me = blockIdx.x;
-  for (int i = tid; i < (int)(sizeof(sh.met) / 4); i += kThreads) sh.met[i] = 0;
+  const bool fill = a.fill_blocks > 0;
+  for (int i = tid; i < kMetWords; i += kThreads) sh.met[i] = 0;
   if (tid == 0) sh.count = 0;
   __syncthreads();
   // Its tokens, 32 at a time, each warp those of its share (they are put in order below).
   for (int t = tid; t < (int)a.rows; t += kThreads) {
-    const int64_t v = tokens[t];
+    const int64_t v = a.tokens[t];
     if (v >= a.vocab && me == 0) atomicOr(a.err, 4u);
     if (v < 0 || v >= a.vocab || (uint32_t)v % B != me) continue;
     const int at = atomicAdd(&sh.count, 1);
@@ -667,27 +676,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  // The rows without tokens: zero, or what the gradient is added to.
-  if (!fill) return;
-  for (uint32_t i = warp; i * (int64_t)B + me < a.vocab; i += kWarps) {
-    if (sh.met[i / 32] >> (i & 31) & 1) continue;
-    const int64_t v = i * (int64_t)B + me;
-    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
-    GT* to = static_cast<GT*>(a.d_table) + v * a.table_stride;
-    const GT* from = static_cast<const GT*>(a.add) + v * a.table_stride;
-    constexpr int kSlabs = 4;
-    for (int s0 = 0; s0 < a.slabs; s0 += kSlabs) {
-      Raw8<GT> x[kSlabs];
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s) {
-        x[s] = {};
-        if (ADD && s0 + s < a.slabs) x[s] = load8<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
-      }
-#pragma unroll
-      for (int s = 0; s < kSlabs; ++s)
-        if (s0 + s < a.slabs) store_raw8<GT, LAY>(to, (s0 + s) * kSlab, lane, a.dim, x[s]);
-    }
-  }
+  if (fill) fill_rows<GT, LAY, ADD>(a, sh.met, me, B);
 }
 
 template <typename TT, typename OT>
@@ -698,71 +687,34 @@ cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
              : launch_kernel(embedding_kernel<TT, OT, kOne>, grid, dim3(kThreads), 0, stream, a);
 }
 
-constexpr int kSortSmem =
-    (int)sizeof(SortShared) + kSortWarps * kMaxDigits * (int)sizeof(uint32_t);
-
-// How many clusters of the sorting kernel the current device runs at the same time
-// (asked once: every variant has the same threads and shared memory).
-cudaError_t clusters_at_once(const void* kernel, int* n) {
-  static std::atomic<int> of_device[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool listed = dev >= 0 && dev < 64;
-  *n = listed ? of_device[dev].load(std::memory_order_relaxed) : 0;
-  if (*n > 0) return cudaSuccess;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kSortBlocks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSortBlocks);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = kSortSmem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
-  if (e == cudaSuccess && listed) of_device[dev].store(*n, std::memory_order_relaxed);
-  return e;
-}
-
 template <typename T, typename GT, Lay LAY>
-cudaError_t launch_sums(const SortArgs& k, const GradArgs& a, cudaStream_t stream) {
-  const bool fill = a.add != a.d_table;
+cudaError_t launch_sums(const SortArgs& k, GradArgs a, cudaStream_t stream) {
+  const int64_t fill = a.add == a.d_table ? 0 : (a.vocab + kWarps - 1) / kWarps;
+  a.fill_blocks = (int32_t)(fill < kFillBlocks ? fill : kFillBlocks);
+  if (k.rows == 0 && !fill) return cudaSuccess;
   if (k.rows > 0 && k.rows <= kFewTokens && k.rows * a.slabs <= kFewItems) {
     // as many blocks as there are rows for their warps, or tokens
-    const int64_t work = fill ? (a.vocab + kWarps - 1) / kWarps : k.rows;
-    const int64_t blocks = work < kFewBlocks ? work : kFewBlocks;
+    const int64_t work = fill ? fill : k.rows;
     return launch_kernel(a.add ? few_tokens_kernel<T, GT, LAY, true>
                                : few_tokens_kernel<T, GT, LAY, false>,
-                         dim3((unsigned)blocks), dim3(kThreads), 0, stream, a, k.tokens, fill);
+                         dim3((unsigned)(work < kFillBlocks ? work : kFillBlocks)),
+                         dim3(kThreads), 0, stream, a);
   }
-  if (k.rows > 0 || fill) {
-    auto* kernel = sort_and_fill_kernel<GT, LAY>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSortSmem);
-    if (e != cudaSuccess) return e;
-    // Fill blocks: as many clusters as run at the same time, the sorting one taken off.
-    int fit = 0;
-    e = clusters_at_once((const void*)kernel, &fit);
-    if (e != cudaSuccess) return e;
-    const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT);
-    const int64_t clusters = (bytes + kSortBlocks * kFillBytes - 1) / (kSortBlocks * kFillBytes);
-    const int64_t most = fit > 1 ? fit - 1 : 1;
-    const int64_t grid = (k.rows > 0 ? kSortBlocks : 0) +
-                         (fill ? kSortBlocks * (clusters < most ? clusters : most) : 0);
-    e = launch_kernel(kernel, dim3((unsigned)grid), dim3(kSortThreads), kSortSmem, stream, k,
-                      a);
+  if (k.rows > 0) {
+    const int smem = (int)sizeof(SortShared) + (kSortWarps * (int)sizeof(uint32_t) << k.bits);
+    cudaError_t e = cudaFuncSetAttribute(sort_tokens_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(SortShared) +
+                                             kSortWarps * kMaxDigits * (int)sizeof(uint32_t));
+    if (e == cudaSuccess)
+      e = launch_kernel(sort_tokens_kernel, dim3(kSortBlocks), dim3(kSortThreads), smem, stream,
+                        k);
     if (e != cudaSuccess) return e;
   }
-  if (k.rows == 0) return cudaSuccess;
-  auto* kernel =
-      a.add ? sum_tokens_kernel<T, GT, LAY, true> : sum_tokens_kernel<T, GT, LAY, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)sizeof(Crossing));
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kernel, dim3((unsigned)(a.blocks * a.slabs)), dim3(kSumThreads),
-                       sizeof(Crossing), stream, a);
+  return launch_kernel(a.add ? embedding_grad_kernel<T, GT, LAY, true>
+                             : embedding_grad_kernel<T, GT, LAY, false>,
+                       dim3((unsigned)(a.fill_blocks + (k.rows > 0 ? a.blocks * a.slabs : 0))),
+                       dim3(kThreads), 0, stream, a);
 }
 
 int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -835,8 +787,10 @@ cudaError_t launch_embedding_grad(const EmbeddingLaunch& in, cudaStream_t stream
   a.scale = (float)in.scale;
   a.err = device_error_word();
   if (!a.err) return cudaErrorInvalidSymbol;
+  a.tokens = in.tokens;
   SortArgs k = {};
   k.rows = in.rows;
+  k.err = a.err;
   k.bits = 1;
   if (in.rows > 0) {
     k.tokens = in.tokens;

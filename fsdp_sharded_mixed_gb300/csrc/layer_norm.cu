@@ -208,8 +208,7 @@ struct RowRing {
   }
   __device__ __forceinline__ void done() { at_work = next(at_work); }
 };
-// The threads that an SM holds of a kernel, by the most of its blocks: 256 for rows
-// of up to four warps or eight, 512, 1024.
+// The threads that an SM holds of a kernel, by the most of its blocks.
 template <int THREADS, int SLABS>
 constexpr int kOfSm = THREADS > 512 ? 1024 : SLABS > 1 ? 512 : THREADS == 512 ? 1024 : 768;
 // Rows in the ring: what those threads hold in 200 KB. 0: rows too wide for one, and
@@ -552,10 +551,10 @@ Shape shape_of(int64_t rows, int64_t dim, bool one) {
   Shape s;
   s.slabs = n <= 4 || (one && n <= 32) ? 1 : n <= 64 ? 2 : 4;
   s.row_warps = (n + s.slabs - 1) / s.slabs;
-  s.block = s.row_warps <= 8 ? 256 : s.row_warps <= 16 ? 512 : 1024;
+  s.block = s.row_warps > 16 ? 1024 : s.slabs > 1 || s.row_warps > 12 ? 512 : 384;
   // few rows are spread over the SMs before they share blocks
   const int64_t each = (rows + 2 * kSMs - 1) / (2 * kSMs);
-  const int64_t most = s.row_warps < 8 ? 8 / s.row_warps : 1;
+  const int64_t most = s.block / 32 / s.row_warps;
   s.groups = (int)(each < 1 ? 1 : each < most ? each : most);
   return s;
 }
@@ -563,16 +562,18 @@ Shape shape_of(int64_t rows, int64_t dim, bool one) {
 int blocks_of(const Shape& s, int64_t rows) {
   const int64_t blocks = (rows + s.groups - 1) / s.groups;
   const int64_t most =
-      kSMs * (s.block > 512 ? 1 : s.slabs > 1 ? 512 / s.block : s.block == 512 ? 2 : 3);
+      kSMs * (s.block > 512 || s.slabs > 1 ? 1 : 2);
   return (int)(blocks < most ? blocks : most);
 }
 
+constexpr int kMostSmem = 208 << 10;  // dynamic shared memory of any of these kernels
 template <typename K>
 cudaError_t launch_rows_kernel(K* kernel, const NormArgs& a, const Shape& s, int smem,
                                cudaStream_t stream) {
   if (smem > 40 << 10) {  // (beside what the kernels declare)
+    // the same for every call: another thread's must not lower it before this one's launch
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(kernel, dim3((unsigned)blocks_of(s, a.rows)), dim3(s.threads()), smem,
@@ -599,10 +600,9 @@ cudaError_t launch_shape(NormArgs a, bool grad, cudaStream_t stream) {
   a.groups = s.groups;
   if (s.slabs == 4) return launch_as<T, LAY, 4, 1024>(a, s, grad, stream);
   if (s.slabs == 2)
-    return s.block == 256   ? launch_as<T, LAY, 2, 256>(a, s, grad, stream)
-           : s.block == 512 ? launch_as<T, LAY, 2, 512>(a, s, grad, stream)
-                            : launch_as<T, LAY, 2, 1024>(a, s, grad, stream);
-  return s.block == 256   ? launch_as<T, LAY, 1, 256>(a, s, grad, stream)
+    return s.block == 512 ? launch_as<T, LAY, 2, 512>(a, s, grad, stream)
+                          : launch_as<T, LAY, 2, 1024>(a, s, grad, stream);
+  return s.block == 384   ? launch_as<T, LAY, 1, 384>(a, s, grad, stream)
          : s.block == 512 ? launch_as<T, LAY, 1, 512>(a, s, grad, stream)
                           : launch_as<T, LAY, 1, 1024>(a, s, grad, stream);
 }

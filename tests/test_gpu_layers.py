@@ -392,8 +392,9 @@ def _step(s, stream=None):
     return [s[k] for k in ("e", "h", "y", "mean", "rstd", "dx", "dw", "db", "dt")]
 
 
-def test_another_stream_and_a_graph_give_the_same_bits():
-    s = _step_buffers(_gen(9))
+@pytest.mark.parametrize("rows,dim", [(200, 192), (3000, 192), (70, 8200)])
+def test_another_stream_and_a_graph_give_the_same_bits(rows, dim):
+    s = _step_buffers(_gen(9), rows, 97, dim)
     want = [t.clone() for t in _step(s)]
     torch.cuda.synchronize()
     stream = torch.cuda.Stream()
@@ -407,7 +408,7 @@ def test_another_stream_and_a_graph_give_the_same_bits():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = _step(s)
-    other = _step_buffers(_gen(10))
+    other = _step_buffers(_gen(10), rows, 97, dim)
     want = [t.clone() for t in _step(other)]
     for name in ("table", "tokens", "w", "b", "dy"):
         s[name].copy_(other[name])
@@ -420,7 +421,7 @@ def test_another_stream_and_a_graph_give_the_same_bits():
 
 
 def test_two_graphs_that_share_a_workspace():
-    a, b = _step_buffers(_gen(11)), _step_buffers(_gen(12), rows=333, vocab=31, dim=96)
+    a, b = _step_buffers(_gen(11), rows=2500), _step_buffers(_gen(12), rows=1333, vocab=31, dim=96)
     want = [[t.clone() for t in _step(s)] for s in (a, b)]
     big = max(a["ws"], b["ws"], key=len)
     a["ws"] = b["ws"] = big
@@ -438,3 +439,29 @@ def test_two_graphs_that_share_a_workspace():
         for i in set(order):
             s = (a, b)[i]
             assert all(torch.equal(s[k], w) for k, w in zip(names, want[i]))
+
+
+def test_many_threads_at_once():
+    """Eight host threads, each on its own stream and buffers, widths whose kernels
+    ask for different amounts of shared memory: each gets what it gets alone."""
+    import threading
+    shapes = [(300, 97, 768), (2000, 31, 768), (40, 9, 4096), (700, 97, 2048), (5, 9, 8192),
+              (900, 50, 768), (1500, 31, 2048), (64, 9, 1000)]
+    sets = [_step_buffers(_gen(20 + i), *x) for i, x in enumerate(shapes)]
+    want = [[t.clone() for t in _step(s)] for s in sets]
+    torch.cuda.synchronize()
+    streams, wrong = [torch.cuda.Stream() for _ in sets], []
+
+    def work(i):
+        for _ in range(30):
+            got = _step(sets[i], stream=streams[i])
+        streams[i].synchronize()
+        if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
