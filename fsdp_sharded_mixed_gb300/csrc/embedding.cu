@@ -232,19 +232,20 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks,
 }
 
 // ---- rows without tokens ----------------------------------------------------------
-// Block b of B owns rows b, b + B, ... of the table; `met` has a bit for each of them,
-// set where the batch has tokens of it.
-constexpr int kFillBlocks = 304;  // two to an SM of 152
+constexpr int kFillBlocks = 304;      // two to an SM of 152
+constexpr int kMostFillBlocks = 1216;
 constexpr int kMetWords = (ZS_MAX_VOCAB / kFillBlocks + 32) / 32;
 
-// Zero, or what the gradient is added to: a warp to a row.
+// A block's rows first, first + step, ...: `met` has a bit for each, set where the
+// batch has tokens of it. The others become zero, or what the gradient is added to: a
+// warp to a row.
 template <typename GT, Lay LAY, bool ADD>
-__device__ __forceinline__ void fill_rows(const GradArgs& a, const uint32_t* met, uint32_t me,
-                                          uint32_t B) {
+__device__ __forceinline__ void fill_rows(const GradArgs& a, const uint32_t* met, uint32_t first,
+                                          uint32_t step, uint32_t rows) {
   const int lane = threadIdx.x & 31;
-  for (uint32_t i = threadIdx.x / 32; i * (int64_t)B + me < a.vocab; i += kWarps) {
+  for (uint32_t i = threadIdx.x / 32; i < rows; i += kWarps) {
     if (met[i / 32] >> (i & 31) & 1) continue;
-    const int64_t v = i * (int64_t)B + me;
+    const int64_t v = first + i * (int64_t)step;
     if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
     GT* to = static_cast<GT*>(a.d_table) + v * a.table_stride;
     const GT* from = static_cast<const GT*>(a.add) + v * a.table_stride;
@@ -542,16 +543,22 @@ __global__ void __launch_bounds__(kThreads, 3)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int i = threadIdx.x; i < kMetWords; i += kThreads) sh.met[i] = 0;
   __syncthreads();
-  const uint32_t B = a.fill_blocks, me = blockIdx.x;
-#pragma unroll 8
-  for (int64_t t = threadIdx.x; t < a.rows; t += kThreads) {
-    const int64_t v = __ldcg(reinterpret_cast<const long long*>(a.tokens) + t);
-    if (v < 0 || v >= a.vocab || (uint32_t)v % B != me) continue;
-    const uint32_t i = (uint32_t)v / B;
-    atomicOr(&sh.met[i / 32], 1u << (i & 31));
+  const uint64_t lo = (uint64_t)a.vocab * blockIdx.x / a.fill_blocks,
+                 hi = (uint64_t)a.vocab * (blockIdx.x + 1) / a.fill_blocks;
+  constexpr int kTokens = 16;  // of a thread, on their way at once
+  for (int64_t t0 = threadIdx.x; t0 < a.rows; t0 += kTokens * kThreads) {
+    uint64_t v[kTokens];
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u) {
+      const int64_t t = t0 + u * kThreads;
+      v[u] = t < a.rows ? __ldcg(reinterpret_cast<const unsigned long long*>(a.tokens) + t) : hi;
+    }
+#pragma unroll
+    for (int u = 0; u < kTokens; ++u)
+      if (v[u] - lo < hi - lo) atomicOr(&sh.met[(v[u] - lo) / 32], 1u << ((v[u] - lo) & 31));
   }
   __syncthreads();
-  fill_rows<GT, LAY, ADD>(a, sh.met, me, B);
+  fill_rows<GT, LAY, ADD>(a, sh.met, (uint32_t)lo, 1, (uint32_t)(hi - lo));
 }
 
 // ---- few tokens -------------------------------------------------------------------
@@ -571,7 +578,7 @@ struct FewShared {
 };
 
 template <typename T, typename GT, Lay LAY, bool ADD>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     few_tokens_kernel(const __grid_constant__ GradArgs a) {
   using R = Reduce<T, GT, LAY, ADD>;
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  if (fill) fill_rows<GT, LAY, ADD>(a, sh.met, me, B);
+  if (fill) fill_rows<GT, LAY, ADD>(a, sh.met, me, B, (a.vocab - 1 - me) / B + 1);
 }
 
 template <typename TT, typename OT>
@@ -689,16 +696,25 @@ cudaError_t launch_lookup(const LookupArgs& a, bool vec, cudaStream_t stream) {
 
 template <typename T, typename GT, Lay LAY>
 cudaError_t launch_sums(const SortArgs& k, GradArgs a, cudaStream_t stream) {
+  // Blocks that write rows: 304, or up to 1216 where a block's rows are many bytes (of
+  // writing and reading) for the 8 a token that it looks through. 304 / 1216: 16384 tokens
+  // of 151936 x 2048 bf16 112 / 106 us, 2048 of 32000 x 4096 fp32 added to another 182 /
+  // 162; but 8191 of 50257 x 768 bf16 added 34.5 / 38.4, 32768 of 32000 x 2048 fp32 73 / 80.
   const int64_t fill = a.add == a.d_table ? 0 : (a.vocab + kWarps - 1) / kWarps;
-  a.fill_blocks = (int32_t)(fill < kFillBlocks ? fill : kFillBlocks);
+  int64_t most = kMostFillBlocks;
+  if (k.rows > 0) {
+    const int64_t bytes = (int64_t)a.vocab * a.dim * (int)sizeof(GT) * (a.add ? 2 : 1);
+    const int64_t worth = bytes / (4 * 8 * k.rows);
+    most = worth < kFillBlocks ? kFillBlocks : worth < most ? worth : most;
+  }
+  a.fill_blocks = (int32_t)(fill < most ? fill : most);
   if (k.rows == 0 && !fill) return cudaSuccess;
   if (k.rows > 0 && k.rows <= kFewTokens && k.rows * a.slabs <= kFewItems) {
     // as many blocks as there are rows for their warps, or tokens
-    const int64_t work = fill ? fill : k.rows;
+    const int64_t work = fill ? a.fill_blocks : k.rows < kFillBlocks ? k.rows : kFillBlocks;
     return launch_kernel(a.add ? few_tokens_kernel<T, GT, LAY, true>
                                : few_tokens_kernel<T, GT, LAY, false>,
-                         dim3((unsigned)(work < kFillBlocks ? work : kFillBlocks)),
-                         dim3(kThreads), 0, stream, a);
+                         dim3((unsigned)work), dim3(kThreads), 0, stream, a);
   }
   if (k.rows > 0) {
     const int smem = (int)sizeof(SortShared) + (kSortWarps * (int)sizeof(uint32_t) << k.bits);
