@@ -10,7 +10,12 @@
 // within a warp's 16 is summed by it; the parts of longer ones and of those that
 // cross warps are added in their order, through shared memory and, across blocks,
 // scratch memory. So the work of a warp is bounded however often a token occurs,
-// and no sum depends on timing.
+// and no sum depends on timing. Sums are fp32; a result is rounded once.
+//
+// Bound: HBM for large tables, which are written whole (16384 tokens of 151936 x
+// 2048 bf16: 106 us, 0.95 of the measured copy rate; 8 tokens: 87, 1.05); latency
+// for middling ones: 8191 of 50257 x 768 added to another matrix 34.7 us (0.71), of
+// which the sort takes 13. The lookup: 16384 rows of 2048 16.1 us (0.86).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -562,7 +567,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // ---- few tokens -------------------------------------------------------------------
-// One launch: block b owns rows b, b + B, ... of the table. It picks its tokens from
+// One launch (512 tokens of 1000 x 256: 5.9 us against 13.9 by sorting; 50 of 50257 x
+// 768 13.6 against 19; 1000 of 50257 x 512 14.6 against 16.5, about where they meet):
+// block b owns rows b, b + B, ... of the table. It picks its tokens from
 // the batch, ranks them by row (counting, in order), writes its rows without tokens
 // and sums the others, 16 tokens a part. For batches whose tokens a block reads at a
 // glance, and whose rows it could sum alone if all went to one of the table's.

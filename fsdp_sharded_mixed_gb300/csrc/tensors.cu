@@ -13,6 +13,11 @@
 // than wait for a last block of the norm's to do it: no ticket to clear, and no
 // launch between the two. It walks the list from its end, where the norm's pass
 // left what L2 still holds.
+//
+// Bound: HBM, with two readings of a list that L2 does not hold, as the norm has to be
+// known before the first element is scaled: 3.09e9 bf16 in 650 tensors 2775 us (0.98
+// of that floor), 152e6 fp32 to bf16 in 218 234 us (0.95). Few small tensors are two
+// launches of latency: 38 in 11 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
