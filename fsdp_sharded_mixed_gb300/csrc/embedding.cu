@@ -161,10 +161,25 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
     uint32_t* od = to_first ? a.order : a.order2;
     for (int i = tid; i < kSortWarps * digits; i += kSortThreads) sh.count[i] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int64_t i = lo + lane; i < hi; i += 32) {
-      const uint32_t key = pass == 0 ? key_of(a, i, err) : __ldcg(ks + i);
-      atomicAdd(&mine[(key >> shift) & (digits - 1)], 1u);
+    // A warp's tokens, 32 * kAtHand at a time; few stay in registers until they are moved.
+    uint32_t keys[kAtHand], from[kAtHand];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int u = 0; u < kAtHand; ++u) {
+        const int64_t i = i0 + u * 32 + lane;
+        const bool some = i < hi;
+        keys[u] = !some ? 0 : pass == 0 ? key_of(a, i, err) : __ldcg(ks + i);
+        from[u] = !some ? 0 : pass == 0 ? (uint32_t)i : __ldcg(os + i);
+      }
+    };
+    const bool held = hi - lo <= 32 * kAtHand;
+    if (held) load(lo);
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAtHand) {
+      if (!held) load(i0);
+#pragma unroll
+      for (int u = 0; u < kAtHand; ++u)
+        if (i0 + u * 32 + lane < hi)
+          atomicAdd(&mine[(keys[u] >> shift) & (digits - 1)], 1u);
     }
     __syncthreads();
     uint32_t total = 0;
@@ -182,6 +197,10 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
         before += r < rank ? n : 0;
         all += n;
       }
+    // (after the last pass nothing is read in this launch: a block may only not leave
+    // before the others have read its counts)
+    const bool ends = pass + 1 == a.passes;
+    if (ends) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     uint32_t upto = all;  // inclusive, over the warp's digits
     for (int off = 1; off < 32; off *= 2) {
       const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, off);
@@ -201,14 +220,7 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
     }
     __syncthreads();
     for (int64_t i0 = lo; i0 < hi; i0 += 32 * kAtHand) {
-      uint32_t keys[kAtHand], from[kAtHand];
-#pragma unroll
-      for (int u = 0; u < kAtHand; ++u) {
-        const int64_t i = i0 + u * 32 + lane;
-        const bool some = i < hi;
-        keys[u] = !some ? 0 : pass == 0 ? key_of(a, i, err) : __ldcg(ks + i);
-        from[u] = !some ? 0 : pass == 0 ? (uint32_t)i : __ldcg(os + i);
-      }
+      if (!held) load(i0);
 #pragma unroll
       for (int u = 0; u < kAtHand; ++u) {
         if (i0 + u * 32 >= hi) break;
@@ -225,7 +237,10 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
         }
       }
     }
-    cluster_sync();  // what was moved is there for all, and the counts have been read
+    if (ends)
+      asm volatile("barrier.cluster.wait;" ::: "memory");
+    else
+      cluster_sync();  // what was moved is there for all, and the counts have been read
   }
 }
 
@@ -240,6 +255,39 @@ __global__ void __launch_bounds__(kSortThreads, 1) __cluster_dims__(kSortBlocks,
 constexpr int kFillBlocks = 304;      // two to an SM of 152
 constexpr int kMostFillBlocks = 1216;
 constexpr int kMetWords = (ZS_MAX_VOCAB / kFillBlocks + 32) / 32;
+
+// The lane's elements, past L1: a block that writes rows beside the sort does not wait
+// for it, and it is that wait which would make sure of what L1 holds.
+template <typename T, Lay LAY>
+__device__ __forceinline__ Raw8<T> load8_from_l2(const T* row, int col0, int lane, int D) {
+  constexpr int kWords = kLane * (int)sizeof(T) / 4;
+  Raw8<T> r;
+  if (LAY == kEight && col0 + lane * 8 + 8 <= D) {
+    const T* p = row + col0 + lane * 8;
+    if (kWords == 8 && (uintptr_t)p % 32 == 0) {
+      asm volatile("ld.relaxed.gpu.global.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]),
+                     "=r"(r.w[kWords - 4]), "=r"(r.w[kWords - 3]), "=r"(r.w[kWords - 2]),
+                     "=r"(r.w[kWords - 1])
+                   : "l"(p)
+                   : "memory");
+      return r;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.w[i]), "=r"(r.w[i + 1]), "=r"(r.w[i + 2]), "=r"(r.w[i + 3])
+                   : "l"(reinterpret_cast<const uint32_t*>(p) + i)
+                   : "memory");
+    return r;
+  }
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    const int c = column<LAY>(col0, lane, k);
+    set_raw(r, k, c < D ? __ldcg(row + c) : T(0.0f));
+  }
+  return r;
+}
 
 // A block's rows first, first + step, ...: `met` has a bit for each, set where the
 // batch has tokens of it. The others become zero, or what the gradient is added to: a
@@ -260,7 +308,8 @@ __device__ __forceinline__ void fill_rows(const GradArgs& a, const uint32_t* met
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s) {
         x[s] = {};
-        if (ADD && s0 + s < a.slabs) x[s] = load8<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
+        if (ADD && s0 + s < a.slabs)
+          x[s] = load8_from_l2<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
       }
 #pragma unroll
       for (int s = 0; s < kSlabs; ++s)
