@@ -14,8 +14,8 @@
 //
 // Bound: HBM for large tables, which are written whole (16384 tokens of 151936 x
 // 2048 bf16: 106 us, 0.95 of the measured copy rate; 8 tokens: 87, 1.05); latency
-// for middling ones: 8191 of 50257 x 768 added to another matrix 34.7 us (0.71), of
-// which the sort takes 13. The lookup: 16384 rows of 2048 16.1 us (0.86).
+// for middling ones: 8191 of 50257 x 768 added to another matrix 33.6 us (0.73), of
+// which the sort takes 10. The lookup: 16384 rows of 2048 16.1 us (0.86).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -295,25 +295,38 @@ __device__ __forceinline__ Raw8<T> load8_from_l2(const T* row, int col0, int lan
 template <typename GT, Lay LAY, bool ADD>
 __device__ __forceinline__ void fill_rows(const GradArgs& a, const uint32_t* met, uint32_t first,
                                           uint32_t step, uint32_t rows) {
+  // (two rows' loads on their way at once where they are few bytes: 8191 tokens of 50257
+  // x 768 bf16 33.6 us against 35.0)
+  constexpr int kSlabs = 4, kRowsAtOnce = ADD && sizeof(GT) == 2 ? 2 : 1;
   const int lane = threadIdx.x & 31;
-  for (uint32_t i = threadIdx.x / 32; i < rows; i += kWarps) {
-    if (met[i / 32] >> (i & 31) & 1) continue;
-    const int64_t v = first + i * (int64_t)step;
-    if (!within(v, v + 1, 0, a.vocab, a.err)) continue;
-    GT* to = static_cast<GT*>(a.d_table) + v * a.table_stride;
-    const GT* from = static_cast<const GT*>(a.add) + v * a.table_stride;
-    constexpr int kSlabs = 4;
+  for (uint32_t i0 = threadIdx.x / 32; i0 < rows; i0 += kRowsAtOnce * kWarps) {
+    bool write[kRowsAtOnce];
+    int64_t at[kRowsAtOnce];
+#pragma unroll
+    for (int k = 0; k < kRowsAtOnce; ++k) {
+      const uint32_t i = i0 + k * kWarps;
+      const int64_t v = first + i * (int64_t)step;
+      write[k] = i < rows && !(met[i / 32] >> (i & 31) & 1) && within(v, v + 1, 0, a.vocab, a.err);
+      at[k] = v * a.table_stride;
+    }
     for (int s0 = 0; s0 < a.slabs; s0 += kSlabs) {
-      Raw8<GT> x[kSlabs];
+      Raw8<GT> x[kRowsAtOnce][kSlabs];
 #pragma unroll
-      for (int s = 0; s < kSlabs; ++s) {
-        x[s] = {};
-        if (ADD && s0 + s < a.slabs)
-          x[s] = load8_from_l2<GT, LAY>(from, (s0 + s) * kSlab, lane, a.dim);
-      }
+      for (int k = 0; k < kRowsAtOnce; ++k)
 #pragma unroll
-      for (int s = 0; s < kSlabs; ++s)
-        if (s0 + s < a.slabs) store_raw8<GT, LAY>(to, (s0 + s) * kSlab, lane, a.dim, x[s]);
+        for (int s = 0; s < kSlabs; ++s) {
+          x[k][s] = {};
+          if (ADD && write[k] && s0 + s < a.slabs)
+            x[k][s] = load8_from_l2<GT, LAY>(static_cast<const GT*>(a.add) + at[k],
+                                             (s0 + s) * kSlab, lane, a.dim);
+        }
+#pragma unroll
+      for (int k = 0; k < kRowsAtOnce; ++k)
+#pragma unroll
+        for (int s = 0; s < kSlabs; ++s)
+          if (write[k] && s0 + s < a.slabs)
+            store_raw8<GT, LAY>(static_cast<GT*>(a.d_table) + at[k], (s0 + s) * kSlab, lane, a.dim,
+                                x[k][s]);
     }
   }
 }

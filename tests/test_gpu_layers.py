@@ -465,3 +465,53 @@ def test_many_threads_at_once():
     for t in threads:
         t.join()
     assert wrong == []
+
+
+@pytest.mark.parametrize("overlap", [1, 0])
+@pytest.mark.parametrize("rows,dim,td", [(3000, 256, F), (2500, 768, B), (200, 320, F)])
+def test_dependent_calls_back_to_back(rows, dim, td, overlap):
+    """Gradients of other tokens into one table, one after another without a wait,
+    each added to the one before or starting anew, and each read by a lookup that
+    follows: as when every call is waited for."""
+    g, vocab, n = _gen(rows), 700, 12
+    tokens = [_tokens(g, rows, vocab, "zipf") for _ in range(n)]
+    d = [_normal(g, rows, dim, dtype=B) for _ in range(n)]
+    ws = torch.empty(zs.zs_embedding_grad_workspace_bytes(rows, dim), dtype=torch.uint8, device=DEV)
+    all_rows = torch.arange(vocab, device=DEV)
+
+    def chain(wait):
+        a, b = torch.zeros(2, vocab, dim, dtype=TYPE[td], device=DEV)
+        outs = []
+        for i in range(n):
+            base = {0: None, 1: a, 2: b}[i % 3]   # anew, in place, added to another
+            zs.zs_embedding_grad(d[i], B, rows, dim, dim, tokens[i], vocab, 1.5, base, ws, a, td, dim)
+            if wait:
+                torch.cuda.synchronize()
+            out = torch.empty(vocab, dim, dtype=TYPE[td], device=DEV)
+            zs.zs_embedding(a, td, vocab, dim, dim, all_rows, vocab, 1.0, out, td, dim)
+            outs.append(out)
+            if i % 3 == 0:
+                b.copy_(a)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    old = zs.zs_set_launch_overlap(overlap)
+    try:
+        want, got = chain(True), chain(False)
+    finally:
+        zs.zs_set_launch_overlap(old)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_launch_overlap_changes_no_bits():
+    s = _step_buffers(_gen(40), rows=2100, vocab=61, dim=768)
+    want = [t.clone() for t in _step(s)]
+    old = zs.zs_set_launch_overlap(0)
+    try:
+        got = _step(s)
+        torch.cuda.synchronize()
+    finally:
+        zs.zs_set_launch_overlap(old)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -182,3 +182,16 @@ def test_graph_and_another_stream():
     graph.replay()
     sq = ref.sqnorm([t.cpu() for t in grads])
     assert abs(o.norm.item() - math.sqrt(sq)) <= (ref.T_SQNORM / 2 + ref.EPS) * math.sqrt(sq)
+
+
+def test_skip_and_coefficient_of_one():
+    grads = _list(8, [5000, 33], F)
+    outs = [torch.full_like(t, 77.0) for t in grads]
+    coef, skip = torch.ones(1, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    zs.zs_tensors_scale(grads, F, coef, skip, outs, F)
+    assert all((t == 77.0).all() for t in outs)
+    skip.zero_()
+    zs.zs_tensors_scale(grads, F, coef, skip, outs, F)
+    assert all(torch.equal(a, b) for a, b in zip(outs, grads))
+    zs.zs_tensors_scale(grads, F, coef * 0.5, None, outs, F)
+    assert all(torch.equal(a, b * 0.5) for a, b in zip(outs, grads))
