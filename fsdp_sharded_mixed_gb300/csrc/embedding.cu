@@ -197,10 +197,11 @@ __device__ void sort_tokens(const SortArgs& a, SortShared& sh, int rank, unsigne
         before += r < rank ? n : 0;
         all += n;
       }
-    // (after the last pass nothing is read in this launch: a block may only not leave
-    // before the others have read its counts)
+    // (What the last pass moves is not read in this launch; a block may only not leave
+    // before the others have read its counts, which they say here. The release makes
+    // sure that they have.)
     const bool ends = pass + 1 == a.passes;
-    if (ends) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    if (ends) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     uint32_t upto = all;  // inclusive, over the warp's digits
     for (int off = 1; off < 32; off *= 2) {
       const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, off);
@@ -473,11 +474,13 @@ __device__ __forceinline__ void sum_tokens(const GradArgs& a, Crossing& sh, int6
   const int slab = (int)(item - b * a.slabs);
   const int64_t p0 = b * kBlock + warp * kEach;
   // the warp's keys, and one to either side
-  const int64_t p = lane == 31 ? p0 - 1 : p0 + lane;
-  const uint32_t here = p >= 0 && p < a.rows ? a.keys[p] : kAll;
-  const uint32_t order = lane < kEach && p < a.rows ? a.order[p] : 0;
-  const uint32_t left = __shfl_sync(kAll, here, (lane + 31) & 31);
-  const uint32_t next = __shfl_sync(kAll, here, kEach);
+  const int64_t p = p0 + lane, q = lane == 0 ? p0 - 1 : p0 + kEach;
+  const bool mine = lane < kEach && p < a.rows;
+  const uint32_t here = mine ? a.keys[p] : kAll;
+  const uint32_t beside = q >= 0 && q < a.rows ? a.keys[q] : kAll;
+  const uint32_t order = mine ? a.order[p] : 0;
+  const uint32_t up = __shfl_up_sync(kAll, here, 1), left = lane == 0 ? beside : up;
+  const uint32_t next = __shfl_sync(kAll, beside, 31);
   // tokens with a row, and the first ones of their runs
   const int n = __popc(__ballot_sync(kAll, lane < kEach && here < (uint32_t)a.vocab));
   const uint32_t starts = __ballot_sync(kAll, lane < n && here != left);
@@ -631,10 +634,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 // ---- few tokens -------------------------------------------------------------------
 // One launch (512 tokens of 1000 x 256: 5.9 us against 13.9 by sorting; 50 of 50257 x
 // 768 13.6 against 19; 1000 of 50257 x 512 14.6 against 16.5, about where they meet):
-// block b owns rows b, b + B, ... of the table. It picks its tokens from
-// the batch, ranks them by row (counting, in order), writes its rows without tokens
-// and sums the others, 16 tokens a part. For batches whose tokens a block reads at a
-// glance, and whose rows it could sum alone if all went to one of the table's.
+// block b owns rows b, b + B, ... of the table. It picks its tokens from the batch,
+// ranks them by row (counting, in order), sums them, 16 a part, and writes its rows
+// without tokens. For batches whose tokens a block reads at a glance, and whose rows
+// it could sum alone if all went to one of the table's.
 constexpr int kFewTokens = 1024;
 constexpr int kFewItems = 2048;  // tokens times slabs
 struct FewShared {
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   for (int i = tid; i < kMetWords; i += kThreads) sh.met[i] = 0;
   if (tid == 0) sh.count = 0;
   __syncthreads();
-  // Its tokens, 32 at a time, each warp those of its share (they are put in order below).
+  // Its tokens, as they come (they are put in order below).
   for (int t = tid; t < (int)a.rows; t += kThreads) {
     const int64_t v = a.tokens[t];
     if (v >= a.vocab && me == 0) atomicOr(a.err, 4u);

@@ -22,8 +22,6 @@ namespace zs {
 constexpr int kSlab = 256;  // columns
 constexpr int kLane = 8;    // elements of a lane in a slab
 
-__device__ __forceinline__ float value_of(float x) { return x; }
-__device__ __forceinline__ float value_of(__nv_bfloat16 x) { return __bfloat162float(x); }
 // The one rounding of a result to its type: to nearest even.
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }

@@ -678,9 +678,9 @@ zs_status zs_layer_norm_grad(const void* d_y, const void* x, zs_dtype dtype, int
  *                     the call returns.
  *   workspace         zs_grad_norm_workspace_bytes() bytes.
  *
- * zs_tensors_sqnorm — *sqnorm_out (device double) = the sum of all squares, of 8 or
- * 16 neighbours in fp32 and then in double; in double throughout where fp32's range
- * does not hold them. */
+ * zs_tensors_sqnorm — *sqnorm_out (device double) = the sum of all squares, 16
+ * (fp32) or 32 (bf16) elements at a time in fp32 and then in double; in double
+ * throughout where fp32's range does not hold them. */
 zs_status zs_tensors_sqnorm(const void* const* tensors, const int64_t* numels, int32_t n,
                             zs_dtype dtype, void* workspace, int64_t workspace_bytes,
                             double* sqnorm_out, void* cuda_stream);
@@ -692,7 +692,7 @@ zs_status zs_tensors_scale(const void* const* tensors, const int64_t* numels, in
                            zs_dtype dtype, const float* coef, const int32_t* skip,
                            void* const* outs, zs_dtype out_dtype, void* cuda_stream);
 /* zs_tensors_clip — both, for gradients that one rank holds whole, with the
- * coefficient between them: *norm_out = sqrt(sum of squares), *coef_out = fp32(min(1,
+ * coefficient between them: *norm_out = fp32(sqrt(sum of squares)), *coef_out = fp32(min(1,
  * max_norm / (norm + 1e-6))), *nonfinite_out = !isfinite(norm), all on the device;
  * a norm that is not finite leaves the outs as they are (and *coef_out = 1).
  * max_norm: finite, > 0. */

@@ -99,7 +99,7 @@ def sqnorm(tensors):
     return sum(float(t.double().square().sum()) for t in tensors)
 
 
-T_SQNORM = 9 * EPS   # eight squares in fp32, then double
+T_SQNORM = 9 * EPS   # chains of eight squares at most, joined twice, in fp32; then double
 
 
 def close(got, ref, tol, what):
