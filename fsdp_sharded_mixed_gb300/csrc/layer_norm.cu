@@ -558,11 +558,13 @@ constexpr int kSMs = 152;  // (fixed, so that the backward pass's sums are)
 
 // One slab a warp up to 1024 columns (8192 x 768 forward 12.4 us, three slabs a warp
 // 16.3) and for rows that start anywhere up to 8192, whose single elements want
-// threads (8191 x 1023 24.9 against 34.1); two up to 8192; four beyond.
+// threads (8191 x 1023 24.9 against 34.1); two up to 8192, three up to
+// 12288 (4096 x 12288 backward 104 us against 134 with four, whose warps are fewer), four
+// beyond.
 Shape shape_of(int64_t rows, int64_t dim, bool one) {
   const int n = (int)((dim + kSlab - 1) / kSlab);
   Shape s;
-  s.slabs = n <= 4 || (one && n <= 32) ? 1 : n <= 32 ? 2 : 4;
+  s.slabs = n <= 4 || (one && n <= 32) ? 1 : n <= 32 ? 2 : n <= 48 ? 3 : 4;
   s.row_warps = (n + s.slabs - 1) / s.slabs;
   s.block = s.row_warps > 16 ? 1024 : s.slabs > 1 || s.row_warps > 12 ? 512 : 384;
   // few rows are spread over the SMs before they share blocks
@@ -614,6 +616,7 @@ cudaError_t launch_shape(NormArgs a, bool grad, cudaStream_t stream) {
   if (s.slabs == 4)
     return s.block == 512 ? launch_as<T, LAY, 4, 512>(a, s, grad, stream)
                           : launch_as<T, LAY, 4, 1024>(a, s, grad, stream);
+  if (s.slabs == 3) return launch_as<T, LAY, 3, 512>(a, s, grad, stream);
   if (s.slabs == 2) return launch_as<T, LAY, 2, 512>(a, s, grad, stream);
   return s.block == 384   ? launch_as<T, LAY, 1, 384>(a, s, grad, stream)
          : s.block == 512 ? launch_as<T, LAY, 1, 512>(a, s, grad, stream)
