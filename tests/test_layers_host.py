@@ -164,8 +164,8 @@ def _array(kind, values):
 
 
 def _list(kind="clip", p=(P, P + 256), n=(8, 8), count=None, dt=F, out=(P + 512, P + 768), od=F,
-          ws=P + 4096, ws_bytes=None, max_norm=1.0, norm=P + 3072, coef=P + 3080, bad=P + 3088,
-          sq=P + 3096):
+          ws=P + 4096, ws_bytes=None, max_norm=1.0, norm=P + 3328, coef=P + 3336, bad=P + 3344,
+          sq=P + 3352):
     import ctypes
     L = zs.lib()
     p = None if p is None else _array(ctypes.c_void_p, p)
@@ -205,7 +205,7 @@ def test_lists_refuse(kind, change, status):
     (dict(out=(P + 256, P + 512)), INVAL),            # another's input
     (dict(out=(P, P + 256), od=B), INVAL),            # in place needs one dtype
     (dict(out=(P, P + 256)), INVAL),                  # in place, but host memory
-    (dict(out=(P + 512, P + 3072)), INVAL),           # the coefficient
+    (dict(out=(P + 512, P + 3328)), INVAL),           # the coefficient
 ])
 def test_lists_refuse_outs(kind, change, status):
     assert _status(lambda: _list(kind, **change)) == status
@@ -216,11 +216,11 @@ def test_lists_refuse_outs(kind, change, status):
     ("clip", dict(max_norm=math.nan), INVAL), ("clip", dict(norm=None), INVAL),
     ("clip", dict(bad=None), INVAL), ("clip", dict(ws=None), INVAL),
     ("clip", dict(ws=P + 4100), ALIGN), ("clip", dict(ws_bytes=16), RANGE),
-    ("clip", dict(norm=P + 3080), INVAL), ("clip", dict(norm=P + 3074), ALIGN),
+    ("clip", dict(norm=P + 3336), INVAL), ("clip", dict(norm=P + 3330), ALIGN),
     ("clip", dict(norm=P + 4), INVAL), ("clip", dict(ws=P), INVAL),
-    ("sqnorm", dict(sq=None), INVAL), ("sqnorm", dict(sq=P + 3092), ALIGN),
+    ("sqnorm", dict(sq=None), INVAL), ("sqnorm", dict(sq=P + 3348), ALIGN),
     ("sqnorm", dict(sq=P + 8), INVAL), ("sqnorm", dict(ws_bytes=0), RANGE),
-    ("scale", dict(coef=P + 3081), ALIGN), ("scale", dict(bad=P + 3081), ALIGN),
+    ("scale", dict(coef=P + 3337), ALIGN), ("scale", dict(bad=P + 3337), ALIGN),
 ])
 def test_lists_refuse_more(kind, change, status):
     assert _status(lambda: _list(kind, **change)) == status
